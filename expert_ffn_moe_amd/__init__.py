@@ -7,8 +7,9 @@ in the library's HIP kernels; if libmoe.so is missing or fails to load, importin
 package raises -- there is no other implementation.
 
 Call names follow the C ABI: route, dispatch, expert_gate_up, expert_gate_up_gather,
-expert_down, expert_ffn, combine, layer, quantize_fp8, plus pack_weights for the one-time
-weight packing.
+expert_down, expert_ffn, combine, layer, quantize_fp8, grouped_linear (with its gradients
+grouped_linear_dx, grouped_linear_dw and activation_backward), plus pack_weights for the
+one-time weight packing.
 
 Problem.dtype "fp8" means FP8 (E4M3, UE8M0 block scales) expert weights with bf16
 activations: pack_weights then takes bf16 weights and quantises them, and the intermediate
@@ -31,6 +32,8 @@ MOE_F32, MOE_BF16, MOE_FP8 = 0, 1, 2
 QBLOCK = 32  # elements per UE8M0 scale
 OP_ROUTE, OP_DISPATCH, OP_FFN, OP_COMBINE, OP_LAYER, OP_ROUTER, OP_BACKWARD = range(7)
 W_GATE_UP, W_DOWN = 0, 1
+OP_GROUPED_LINEAR, OP_GROUPED_DX, OP_GROUPED_DW = range(3)
+ACTIVATIONS = {"none": 0, "relu": 1, "relu2": 2, "silu": 3, "gelu_tanh": 4}
 
 EXPORTS = ("moe_status_str", "moe_problem_check", "moe_workspace_bytes", "moe_packed_bytes",
            "moe_pack_weights", "moe_route", "moe_dispatch", "moe_expert_ffn", "moe_expert_gate_up",
@@ -39,7 +42,9 @@ EXPORTS = ("moe_status_str", "moe_problem_check", "moe_workspace_bytes", "moe_pa
            "moe_route_grouped", "moe_router", "moe_layer_chunked_workspace_bytes",
            "moe_layer_chunked", "moe_pack_weights_backward", "moe_expert_gate_up_gather_gu",
            "moe_layer_backward", "moe_debug_status", "moe_layer_static",
-           "moe_layer_static_max_bytes")
+           "moe_layer_static_max_bytes", "moe_grouped_check", "moe_grouped_workspace_bytes",
+           "moe_grouped_linear", "moe_grouped_linear_dx", "moe_grouped_linear_dw",
+           "moe_activation_backward")
 
 
 class MoeError(RuntimeError):
@@ -68,6 +73,10 @@ class MoeProblem(ctypes.Structure):
                 ("T", "H", "E", "k", "I", "capacity", "renormalize", "act_dtype", "w_dtype")]
 
 
+class MoeGrouped(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("R", "T", "K", "N", "E")]
+
+
 def _load(path: str = LIB_PATH) -> ctypes.CDLL:
     if not os.path.exists(path):
         raise ImportError(f"{path} is not built; run `python expert_ffn_moe_amd/build.py` "
@@ -75,6 +84,8 @@ def _load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib = ctypes.CDLL(path)
     P = ctypes.c_void_p
     PP = ctypes.POINTER(MoeProblem)
+    PG = ctypes.POINTER(MoeGrouped)
+    i32, i64 = ctypes.c_int32, ctypes.c_int64
     sz = ctypes.c_size_t
     sigs = {
         "moe_status_str": (ctypes.c_char_p, [ctypes.c_int]),
@@ -106,6 +117,13 @@ def _load(path: str = LIB_PATH) -> ctypes.CDLL:
         "moe_debug_status": (ctypes.c_int, [ctypes.POINTER(ctypes.c_uint32)]),
         "moe_layer_static": (ctypes.c_int, [PP, P, P, P, P, P, P, P, P, P, P, P, P, P]),
         "moe_layer_static_max_bytes": (ctypes.c_size_t, []),
+        "moe_grouped_check": (ctypes.c_int, [PG]),
+        "moe_grouped_workspace_bytes": (sz, [PG, ctypes.c_int]),
+        "moe_grouped_linear": (ctypes.c_int, [PG, P, P, P, P, P, ctypes.c_int, P, P, P, P, P, sz,
+                                              P]),
+        "moe_grouped_linear_dx": (ctypes.c_int, [PG, P, P, P, ctypes.c_int, P, P, P, P, P, sz, P]),
+        "moe_grouped_linear_dw": (ctypes.c_int, [PG, P, P, P, P, ctypes.c_int, P, P, P, sz, P]),
+        "moe_activation_backward": (ctypes.c_int, [i64, i32, P, ctypes.c_int, P, P, P, P, P, P]),
     }
     for name, (res, args) in sigs.items():
         fn = getattr(lib, name)
@@ -550,3 +568,159 @@ def routing_buffers(p: Problem, device="cuda"):
                 offsets=_empty((p.E + 1,), torch.int32, device),
                 row_token=_empty((tk,), torch.int32, device),
                 slot_to_row=_empty((p.T, p.k), torch.int32, device))
+
+
+# ---- grouped linear products (see moe_grouped_linear and the calls after it in include/moe.h)
+@dataclasses.dataclass(frozen=True)
+class GroupedProblem:
+    """Shapes of a grouped linear product: R rows in the layout, K -> N, E experts; T: rows of
+    x when it is read through row_token (default R)."""
+    R: int
+    K: int
+    N: int
+    E: int = 1
+    T: Optional[int] = None
+
+    def c(self) -> MoeGrouped:
+        return MoeGrouped(self.R, self.x_tokens, self.K, self.N, self.E)
+
+    @property
+    def x_tokens(self) -> int:
+        return self.R if self.T is None else self.T
+
+    def check(self) -> int:
+        c = self.c()
+        return lib.moe_grouped_check(ctypes.byref(c))
+
+    def workspace_bytes(self, op: int) -> int:
+        c = self.c()
+        return int(lib.moe_grouped_workspace_bytes(ctypes.byref(c), op))
+
+
+def grouped_workspace(p: GroupedProblem, op: int, device="cuda"):
+    """A workspace buffer for `op` (OP_GROUPED_*), or None if it needs none."""
+    n = p.workspace_bytes(op)
+    return torch.empty(n, dtype=torch.uint8, device=device) if n else None
+
+
+def checkpoint_buffers(rows: int, cols: int, device="cuda"):
+    """Buffers (codes [rows, cols], scales [rows, cols/32]) of an 8-bit checkpoint."""
+    if cols % QBLOCK:
+        raise ValueError(f"a checkpoint's width is a multiple of {QBLOCK}, not {cols}")
+    return (_empty((rows, cols), torch.uint8, device),
+            _empty((rows, cols // QBLOCK), torch.uint8, device))
+
+
+def _act(name: str) -> int:
+    if name not in ACTIVATIONS:
+        raise ValueError(f"unknown activation {name!r}; one of {', '.join(ACTIVATIONS)}")
+    return ACTIVATIONS[name]
+
+
+def _need_all(first: torch.Tensor, **named):
+    """named: (tensor or None, shape, dtype); all on the device of `first`."""
+    for name, (t, shape, dtype) in named.items():
+        if t is not None:
+            _need(t, name, shape, dtype)
+            if t.device != first.device:
+                raise ValueError(f"{name} is on {t.device}, expected {first.device}")
+
+
+def _grouped_call(name: str, p: GroupedProblem, op: int, ws, device, *args):
+    """The call on the current stream of the tensors' device, with a workspace if it needs one."""
+    if ws is None:
+        ws = grouped_workspace(p, op, device)
+    elif ws.device != device or ws.dtype != torch.uint8 or not ws.is_contiguous():
+        raise ValueError(f"ws must be a contiguous uint8 tensor on {device}")
+    c = p.c()
+    with torch.cuda.device(device):
+        _call(name, ctypes.byref(c), *args, _ptr(ws), 0 if ws is None else ws.numel(), _stream())
+
+
+def _grouped_common(p: GroupedProblem, offsets):
+    if offsets is None and p.E != 1:
+        raise ValueError("offsets may be left out only with one expert")
+    return (offsets, (p.E + 1,), torch.int32)
+
+
+def grouped_linear(p: GroupedProblem, x, w, offsets=None, bias=None, act: str = "none",
+                   residual=None, row_token=None, checkpoint=None, out=None, ws=None):
+    """y[r] = act(x[r] w[e] + bias[e]) + residual[r] for the rows of each expert (x [R, K], or
+    [T, K] read through row_token).  checkpoint: None, or the (codes, scales) buffers that
+    receive the pre-activations in 8 bits.  Returns y [R, N]; rows behind the last expert's
+    are left as they were."""
+    bf = torch.bfloat16
+    codes, scales = checkpoint if checkpoint is not None else (None, None)
+    _need(x, "x", (p.R if row_token is None else p.x_tokens, p.K), bf)
+    y = _empty((p.R, p.N), bf, x.device) if out is None else out
+    _need_all(x, w=(w, (p.E, p.K, p.N), bf), offsets=_grouped_common(p, offsets),
+              bias=(bias, (p.E, p.N), bf), residual=(residual, (p.R, p.N), bf),
+              row_token=(row_token, (p.R,), torch.int32), out=(y, (p.R, p.N), bf),
+              codes=(codes, (p.R, p.N), torch.uint8),
+              scales=(scales, (p.R, p.N // QBLOCK), torch.uint8))
+    _grouped_call("moe_grouped_linear", p, OP_GROUPED_LINEAR, ws, x.device, _ptr(x),
+                  _ptr(row_token), _ptr(offsets), _ptr(w), _ptr(bias), _act(act),
+                  _ptr(residual), _ptr(y), _ptr(codes), _ptr(scales))
+    return y
+
+
+def grouped_linear_dx(p: GroupedProblem, dz, w, offsets=None, act: str = "none",
+                      checkpoint=None, out=None, a=None, ws=None):
+    """dx[r] = (dz[r] w[e]^T) * act'(z[r]) with z [R, K] from the checkpoint of the product
+    whose activation made x (None: dz w^T alone); a, if given, receives act(z) [R, K].
+    Returns dx [R, K]."""
+    bf = torch.bfloat16
+    codes, scales = checkpoint if checkpoint is not None else (None, None)
+    _need(dz, "dz", (p.R, p.N), bf)
+    dx = _empty((p.R, p.K), bf, dz.device) if out is None else out
+    _need_all(dz, w=(w, (p.E, p.K, p.N), bf), offsets=_grouped_common(p, offsets),
+              codes=(codes, (p.R, p.K), torch.uint8),
+              scales=(scales, (p.R, p.K // QBLOCK), torch.uint8), out=(dx, (p.R, p.K), bf),
+              a=(a, (p.R, p.K), bf))
+    _grouped_call("moe_grouped_linear_dx", p, OP_GROUPED_DX, ws, dz.device, _ptr(dz),
+                  _ptr(offsets), _ptr(w), _act(act), _ptr(codes), _ptr(scales), _ptr(dx),
+                  _ptr(a))
+    return dx
+
+
+def grouped_linear_dw(p: GroupedProblem, x, dz, offsets=None, row_token=None,
+                      want_bias: bool = False, dw=None, dbias=None, accumulate: bool = False,
+                      ws=None):
+    """dw[e] = x_e^T dz_e [E, K, N] and dbias[e] = the column sums of dz_e [E, N], in fp32
+    (accumulate: added to what dw and dbias hold, which must be given).  Returns (dw, dbias);
+    dbias None unless asked for or passed in."""
+    bf, f32 = torch.bfloat16, torch.float32
+    _need(x, "x", (p.R if row_token is None else p.x_tokens, p.K), bf)
+    if accumulate and (dw is None or (want_bias and dbias is None)):
+        raise ValueError("accumulate needs the gradients to add to")
+    dw = _empty((p.E, p.K, p.N), f32, x.device) if dw is None else dw
+    if dbias is None and want_bias:
+        dbias = _empty((p.E, p.N), f32, x.device)
+    _need_all(x, dz=(dz, (p.R, p.N), bf), offsets=_grouped_common(p, offsets),
+              row_token=(row_token, (p.R,), torch.int32), dw=(dw, (p.E, p.K, p.N), f32),
+              dbias=(dbias, (p.E, p.N), f32))
+    _grouped_call("moe_grouped_linear_dw", p, OP_GROUPED_DW, ws, x.device, _ptr(x),
+                  _ptr(row_token), _ptr(dz), _ptr(offsets), int(bool(accumulate)), _ptr(dw),
+                  _ptr(dbias))
+    return dw, dbias
+
+
+def activation_backward(dy, checkpoint, act: str, live_rows=None, out=None, a=None):
+    """dz = dy * act'(z) with z from an 8-bit checkpoint; a, if given, receives act(z).
+    live_rows: an i32 tensor of one element (offsets[-1:]); rows behind it are left as they
+    were.  Returns dz, shaped as dy [rows, cols]."""
+    if dy.dim() != 2:
+        raise ValueError("dy must be 2-D")
+    bf = torch.bfloat16
+    rows, cols = dy.shape
+    codes, scales = checkpoint
+    _need(dy, "dy", (rows, cols), bf)
+    dz = _empty((rows, cols), bf, dy.device) if out is None else out
+    _need_all(dy, codes=(codes, (rows, cols), torch.uint8),
+              scales=(scales, (rows, cols // QBLOCK), torch.uint8), out=(dz, (rows, cols), bf),
+              a=(a, (rows, cols), bf), live_rows=(live_rows, (1,), torch.int32))
+    with torch.cuda.device(dy.device):
+        _call("moe_activation_backward", ctypes.c_int64(rows), ctypes.c_int32(cols),
+              _ptr(live_rows), _act(act), _ptr(dy), _ptr(codes), _ptr(scales), _ptr(dz), _ptr(a),
+              _stream())
+    return dz

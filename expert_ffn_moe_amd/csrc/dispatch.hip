@@ -343,6 +343,21 @@ __global__ __launch_bounds__(256) void check_ids_kernel(const int32_t* __restric
   }
   if (bad) atomicOr(&g_debug_status, bad);
 }
+
+// Bit 2: offsets that decrease or leave [0, R]; bit 3: a row_token outside [0, T).
+__global__ __launch_bounds__(256) void check_grouped_kernel(const int32_t* __restrict__ offsets,
+                                                            const int32_t* __restrict__ row_token,
+                                                            int R, int T, int E) {
+  const int i = blockIdx.x * 256 + threadIdx.x;
+  unsigned int bad = 0;
+  if (offsets && i <= E) {
+    const int o = offsets[i];
+    if (o < 0 || o > R || (i > 0 && o < offsets[i - 1])) bad |= 4u;
+  }
+  const int n = offsets ? min(offsets[E], R) : R;
+  if (row_token && i < n && (row_token[i] < 0 || row_token[i] >= T)) bad |= 8u;
+  if (bad) atomicOr(&g_debug_status, bad);
+}
 #endif
 
 }  // namespace
@@ -415,6 +430,14 @@ hipError_t launch_gather(const moe_problem& p, const void* x, const int32_t* slo
 hipError_t launch_check_ids(const moe_problem& p, const int32_t* ids, hipStream_t s) {
   hipLaunchKernelGGL(check_ids_kernel, dim3(div_up(p.T, 256)), dim3(256), 0, s, ids, p.T, p.k,
                      p.E);
+  return hipGetLastError();
+}
+
+hipError_t launch_check_grouped(const moe_grouped& g, const int32_t* offsets,
+                                const int32_t* row_token, hipStream_t s) {
+  const int n = std::max(row_token ? g.R : 0, g.E + 1);
+  hipLaunchKernelGGL(check_grouped_kernel, dim3(div_up(n, 256)), dim3(256), 0, s, offsets,
+                     row_token, g.R, g.T, g.E);
   return hipGetLastError();
 }
 

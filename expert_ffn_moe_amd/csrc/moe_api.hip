@@ -403,6 +403,42 @@ void* static_scratch() {
   return g_scratch_ptr[dev];
 }
 
+// ---- grouped linear products
+constexpr int kCkptBlock = 32;  // columns per scale of an 8-bit checkpoint
+bool act_ok(int act) { return act >= MOE_ACT_NONE && act <= MOE_ACT_GELU_TANH; }
+size_t rows_bf16(size_t rows, size_t cols) { return rows * cols * 2; }
+size_t grouped_w(const moe_grouped& g) { return (size_t)g.E * g.K * g.N; }
+// One output tile per expert and 64 x 64 block at most: their number stays an int.
+bool grouped_tiles_ok(const moe_grouped& g) {
+  const int64_t mt = (int64_t)g.R / 64 + g.E, kt = div_up(g.K, 64), nt = div_up(g.N, 64);
+  const int64_t lim = INT32_MAX;
+  return mt * std::max(kt, nt) < lim && (int64_t)g.E * kt < lim / nt;
+}
+// NULL offsets name one expert; every pointer that is there is 16-byte aligned.
+bool grouped_args_ok(const moe_grouped& g, const int32_t* offsets,
+                     std::initializer_list<const void*> ptrs) {
+  if (!offsets && g.E != 1) return false;
+  for (const void* q : ptrs)
+    if (!aligned16(q)) return false;
+  return true;
+}
+size_t grouped_ws_bytes(const moe_grouped& g, int op) { return 0; }
+int check_grouped_ws(const moe_grouped& g, int op, const void* ws, size_t ws_bytes) {
+  const size_t need = grouped_ws_bytes(g, op);
+  if (need == 0) return MOE_OK;
+  if (!ws) return MOE_ERR_WORKSPACE;
+  if (((uintptr_t)ws & 255) != 0) return MOE_ERR_INVALID_ARG;
+  return ws_bytes < need ? MOE_ERR_WORKSPACE : MOE_OK;
+}
+// Debug builds report bad offsets and row indices.
+hipError_t check_grouped_device(const moe_grouped& g, const int32_t* offsets,
+                                const int32_t* row_token, hipStream_t s) {
+#ifdef MOE_DEBUG_CHECKS
+  if (offsets || row_token) return launch_check_grouped(g, offsets, row_token, s);
+#endif
+  return hipSuccess;
+}
+
 }  // namespace
 
 extern "C" {
@@ -903,6 +939,105 @@ int moe_debug_status(uint32_t* status) {
 #else
   return MOE_ERR_UNSUPPORTED;
 #endif
+}
+
+int moe_grouped_check(const moe_grouped* g) {
+  if (!g || g->R < 0 || g->T < 0 || g->K < 1 || g->N < 1 || g->E < 1) return MOE_ERR_INVALID_ARG;
+  if (g->E > kMaxE || g->K % 8 || g->N % 8 || g->K > (1 << 20) || g->N > (1 << 20) ||
+      g->R > (1 << 30))
+    return MOE_ERR_UNSUPPORTED;
+  return grouped_tiles_ok(*g) ? MOE_OK : MOE_ERR_UNSUPPORTED;
+}
+
+size_t moe_grouped_workspace_bytes(const moe_grouped* g, int op) {
+  if (moe_grouped_check(g) != MOE_OK || op < MOE_GROUPED_LINEAR || op > MOE_GROUPED_DW) return 0;
+  return grouped_ws_bytes(*g, op);
+}
+
+int moe_grouped_linear(const moe_grouped* g, const void* x, const int32_t* row_token,
+                       const int32_t* offsets, const void* w, const void* bias, int act,
+                       const void* residual, void* y, uint8_t* z_codes, uint8_t* z_scales,
+                       void* ws, size_t ws_bytes, void* stream) {
+  int st = moe_grouped_check(g);
+  if (st != MOE_OK) return st;
+  if (!grouped_args_ok(*g, offsets, {x, w, bias, residual, y, z_codes}) || !w ||
+      (g->R > 0 && (!x || !y)) || !act_ok(act) || !z_codes != !z_scales)
+    return MOE_ERR_INVALID_ARG;
+  if (z_codes && g->N % kCkptBlock) return MOE_ERR_UNSUPPORTED;
+  const size_t yb = rows_bf16(g->R, g->N);
+  if (aliased({{y, yb}, {z_codes, yb / 2}, {z_scales, yb / 2 / kCkptBlock}, {ws, ws_bytes}},
+              {{x, rows_bf16(row_token ? g->T : g->R, g->K)}, {row_token, (size_t)g->R * 4},
+               {offsets, ((size_t)g->E + 1) * 4}, {w, grouped_w(*g) * 2},
+               {bias, rows_bf16(g->E, g->N)}, {residual, yb}}))
+    return MOE_ERR_INVALID_ARG;
+  if ((st = check_grouped_ws(*g, MOE_GROUPED_LINEAR, ws, ws_bytes)) != MOE_OK) return st;
+  if (g->R == 0) return MOE_OK;
+  hipError_t err = check_grouped_device(*g, offsets, row_token, as_stream(stream));
+  if (err == hipSuccess)
+    err = launch_grouped_linear(*g, x, row_token, offsets, w, bias, act, residual, y, z_codes,
+                                z_scales, as_stream(stream));
+  return status_of(err);
+}
+
+int moe_grouped_linear_dx(const moe_grouped* g, const void* dz, const int32_t* offsets,
+                          const void* w, int act, const uint8_t* z_codes,
+                          const uint8_t* z_scales, void* dx, void* a, void* ws,
+                          size_t ws_bytes, void* stream) {
+  int st = moe_grouped_check(g);
+  if (st != MOE_OK) return st;
+  if (!grouped_args_ok(*g, offsets, {dz, w, z_codes, dx, a}) || !w ||
+      (g->R > 0 && (!dz || !dx)) || !act_ok(act) || !z_codes != !z_scales ||
+      (g->R > 0 && !z_codes && (a || act != MOE_ACT_NONE)))
+    return MOE_ERR_INVALID_ARG;
+  if (z_codes && g->K % kCkptBlock) return MOE_ERR_UNSUPPORTED;
+  const size_t xb = rows_bf16(g->R, g->K);
+  if (aliased({{dx, xb}, {a, xb}, {ws, ws_bytes}},
+              {{dz, rows_bf16(g->R, g->N)}, {offsets, ((size_t)g->E + 1) * 4},
+               {w, grouped_w(*g) * 2}, {z_codes, xb / 2}, {z_scales, xb / 2 / kCkptBlock}}))
+    return MOE_ERR_INVALID_ARG;
+  if ((st = check_grouped_ws(*g, MOE_GROUPED_DX, ws, ws_bytes)) != MOE_OK) return st;
+  if (g->R == 0) return MOE_OK;
+  hipError_t err = check_grouped_device(*g, offsets, nullptr, as_stream(stream));
+  if (err == hipSuccess)
+    err = launch_grouped_dx(*g, dz, offsets, w, act, z_codes, z_scales, dx, a, as_stream(stream));
+  return status_of(err);
+}
+
+int moe_grouped_linear_dw(const moe_grouped* g, const void* x, const int32_t* row_token,
+                          const void* dz, const int32_t* offsets, int accumulate, float* dw,
+                          float* dbias, void* ws, size_t ws_bytes, void* stream) {
+  int st = moe_grouped_check(g);
+  if (st != MOE_OK) return st;
+  if (!grouped_args_ok(*g, offsets, {x, dz, dw, dbias}) || !dw || (g->R > 0 && (!x || !dz)) ||
+      (accumulate != 0 && accumulate != 1))
+    return MOE_ERR_INVALID_ARG;
+  if (aliased({{dw, grouped_w(*g) * 4}, {dbias, (size_t)g->E * g->N * 4}, {ws, ws_bytes}},
+              {{x, rows_bf16(row_token ? g->T : g->R, g->K)}, {row_token, (size_t)g->R * 4},
+               {dz, rows_bf16(g->R, g->N)}, {offsets, ((size_t)g->E + 1) * 4}}))
+    return MOE_ERR_INVALID_ARG;
+  if ((st = check_grouped_ws(*g, MOE_GROUPED_DW, ws, ws_bytes)) != MOE_OK) return st;
+  hipError_t err = check_grouped_device(*g, offsets, row_token, as_stream(stream));
+  if (err == hipSuccess)
+    err = launch_grouped_dw(*g, x, row_token, dz, offsets, accumulate, dw, dbias,
+                            as_stream(stream));
+  return status_of(err);
+}
+
+int moe_activation_backward(int64_t rows, int32_t cols, const int32_t* live_rows, int act,
+                            const void* dy, const uint8_t* z_codes, const uint8_t* z_scales,
+                            void* dz, void* a, void* stream) {
+  if (rows < 0 || rows > ((int64_t)1 << 40) || cols < 1 || cols % kCkptBlock || !act_ok(act) ||
+      (rows > 0 && (!dy || !z_codes || !z_scales || !dz)))
+    return MOE_ERR_INVALID_ARG;
+  if (!aligned16(dy) || !aligned16(z_codes) || !aligned16(dz) || !aligned16(a))
+    return MOE_ERR_INVALID_ARG;
+  const size_t n = (size_t)rows * cols;
+  if (aliased({{dz, 2 * n}, {a, 2 * n}},
+              {{dy, 2 * n}, {z_codes, n}, {z_scales, n / kCkptBlock}, {live_rows, 4}}))
+    return MOE_ERR_INVALID_ARG;
+  if (rows == 0) return MOE_OK;
+  return status_of(launch_act_backward(rows, cols, live_rows, act, dy, z_codes, z_scales, dz, a,
+                                       as_stream(stream)));
 }
 
 size_t moe_layer_chunked_workspace_bytes(const moe_problem* p, int32_t chunk_tokens,

@@ -11,6 +11,9 @@
  *   moe_layer_chunked  the layer over chunks of tokens, layouts on a second stream,
  *                    optional shared expert
  *   moe_layer_backward gradients of the layer (x, expert weights, logits, router)
+ *   moe_grouped_linear  one product per expert over its rows, with bias, activation and
+ *                    residual, and its gradients (moe_grouped_linear_dx, _dw,
+ *                    moe_activation_backward) from pre-activations kept in 8 bits
  *
  * The pages describe the operations in prose; each declaration names the passage:
  *   [axolotl]  docs.axolotl.ai "integrations.expert_parallel.args", attribute table
@@ -111,7 +114,8 @@ const char* moe_status_str(int status);
 /* Debug library only ([axolotl] `validate_expert_parallel_topology`: what the kernels cannot
  * handle is reported, never run another way): waits for the current device, writes the
  * sticky status word of its precondition checks to *status and clears it.  Bit 0: an expert
- * id outside [0, E) was passed; bit 1: a token's k ids were not distinct.  The release
+ * id outside [0, E) was passed; bit 1: a token's k ids were not distinct; bit 2: grouped
+ * offsets that decrease or leave [0, R]; bit 3: a row_token outside [0, T).  The release
  * library sets *status = 0 and returns MOE_ERR_UNSUPPORTED; MOE_ERR_INVALID_ARG if status
  * is NULL. */
 int moe_debug_status(uint32_t* status);
@@ -433,6 +437,115 @@ int moe_layer_backward(const moe_problem* p, const void* x, const float* logits,
                        const void* packed_bwd_down, const moe_saved_routing* saved,
                        const void* yp, const void* gu, const void* dy,
                        const moe_grads* grads, void* ws, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------------
+ * Grouped linear products -- the building block of experts that are not the SwiGLU FFN above
+ * (biases, other activations, a residual) and, with E = 1, of the dense layers around
+ * them; with the gradients, for training.  The weights stay in their natural layout
+ * [E, K, N] (y = x W): nothing is packed, so weights that change every step can be used as
+ * they are.  Rows are those of the prefix-sum layout: expert e owns rows offsets[e] ..
+ * offsets[e + 1] - 1 (offsets from moe_dispatch).  offsets may be NULL when E = 1: all R rows
+ * belong to the one expert.  Rows >= offsets[E] are neither read nor written.
+ *
+ * Everything is bf16 (fp32 accumulation, each stored bf16 value rounded once) except the
+ * weight and bias gradients, which are fp32.  Every result is deterministic.
+ * The kernels take offsets as clamped to [0, R], and read zeros for a row whose row_token
+ * lies outside [0, T); the debug library reports both (moe_debug_status bits 2 and 3).
+ *
+ *   R     rows the row buffers hold (0: they may be NULL and nothing is enqueued, except that
+ *         moe_grouped_linear_dw still clears its outputs)
+ *   T     rows of x when they are read through row_token (ignored without row_token)
+ *   K, N  input and output width: multiples of 8
+ *   E     experts, at most 1024
+ * --------------------------------------------------------------------------------- */
+typedef struct {
+  int32_t R, T, K, N, E;
+} moe_grouped;
+
+/* relu2 is max(z, 0)^2; gelu is in its tanh form, z / (1 + exp(-2 u)) with
+ * u = sqrt(2 / pi) (z + 0.044715 z^3). */
+typedef enum {
+  MOE_ACT_NONE = 0,
+  MOE_ACT_RELU = 1,
+  MOE_ACT_RELU2 = 2,
+  MOE_ACT_SILU = 3,
+  MOE_ACT_GELU_TANH = 4
+} moe_activation;
+
+typedef enum {
+  MOE_GROUPED_LINEAR = 0,
+  MOE_GROUPED_DX = 1,
+  MOE_GROUPED_DW = 2
+} moe_grouped_op;
+
+/* MOE_OK, MOE_ERR_INVALID_ARG (g NULL, R or T < 0, K, N or E < 1) or MOE_ERR_UNSUPPORTED
+ * (E > 1024, K or N not a multiple of 8 or above 2^20, R > 2^30, or more tiles than 2^31). */
+int moe_grouped_check(const moe_grouped* g);
+
+/* Workspace bytes of `op` (a moe_grouped_op) for g: partial sums where few tiles are split
+ * along a long reduction.  0 if none is needed or g is invalid. */
+size_t moe_grouped_workspace_bytes(const moe_grouped* g, int op);
+
+/* ---------------------------------------------------------------------------------
+ * moe_grouped_linear -- with z[r] = x[r'] W[e] + bias[e], r' = row_token ? row_token[r] : r:
+ *   y[r] = act(z[r]) + residual[r]
+ *   x        [R, K] (or [T, K] with row_token [R] i32)
+ *   w        [E, K, N]
+ *   bias     [E, N] or NULL
+ *   residual [R, N] or NULL
+ *   y        [R, N]
+ *   z_codes  [R, N] u8, z_scales [R, N/32] u8, both or neither: receive z as an 8-bit
+ *            checkpoint in the format of moe_quantize_fp8 (rounded from the fp32 z; a z that
+ *            is not finite becomes the NaN code and does not count for its block's scale).
+ *            1.03 bytes per value against 2 of a bf16 copy.
+ * All pointers 16-byte aligned (z_scales and the i32 arrays: naturally).
+ * MOE_ERR_UNSUPPORTED with a checkpoint unless N % 32 == 0.
+ * --------------------------------------------------------------------------------- */
+int moe_grouped_linear(const moe_grouped* g, const void* x, const int32_t* row_token,
+                       const int32_t* offsets, const void* w, const void* bias, int act,
+                       const void* residual, void* y, uint8_t* z_codes, uint8_t* z_scales,
+                       void* ws, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------------
+ * moe_grouped_linear_dx -- the data gradient of that product, carried on through the
+ * activation that made its input:
+ *   dx[r] = (dz[r] W[e]^T) * act'(z[r]),   a[r] = act(z[r])
+ *   dz [R, N], w [E, K, N], dx [R, K]
+ *   z_codes [R, K], z_scales [R, K/32]: the checkpoint of the product before (whose output
+ *     act(z) was this product's x), or NULL with act MOE_ACT_NONE: dx is dz W^T alone.
+ *   a  [R, K] or NULL: receives act(z), the x that moe_grouped_linear_dw needs, so that the
+ *     forward need not keep it (only with a checkpoint).
+ * dx stays in the layout's row order; moe_combine with weights 1 sums the rows of a token.
+ * MOE_ERR_UNSUPPORTED with a checkpoint unless K % 32 == 0.
+ * --------------------------------------------------------------------------------- */
+int moe_grouped_linear_dx(const moe_grouped* g, const void* dz, const int32_t* offsets,
+                          const void* w, int act, const uint8_t* z_codes,
+                          const uint8_t* z_scales, void* dx, void* a, void* ws,
+                          size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------------
+ * moe_grouped_linear_dw -- the weight and bias gradients, summed over each expert's rows:
+ *   dw[e] = sum over r of x[r']^T dz[r],   dbias[e] = sum over r of dz[r]
+ *   x, row_token as moe_grouped_linear; dz [R, N]; dw [E, K, N] f32; dbias [E, N] f32 or NULL
+ *   accumulate 0: dw and dbias are written (zeros for an expert without rows);
+ *              1: the sums are added to what they hold (the micro-batches of a step).
+ * --------------------------------------------------------------------------------- */
+int moe_grouped_linear_dw(const moe_grouped* g, const void* x, const int32_t* row_token,
+                          const void* dz, const int32_t* offsets, int accumulate, float* dw,
+                          float* dbias, void* ws, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------------
+ * moe_activation_backward -- the activation's gradient at a product whose output leaves the
+ * experts (no product follows whose moe_grouped_linear_dx could carry it):
+ *   dz[r] = dy[r] * act'(z[r]),   a[r] = act(z[r])       for r < *live_rows
+ *   dy, dz [rows, cols] bf16; z_codes [rows, cols], z_scales [rows, cols/32]; a [rows, cols]
+ *   bf16 or NULL; live_rows: device pointer (offsets + E), or NULL: all rows.
+ * rows = 0 enqueues nothing.  MOE_ERR_INVALID_ARG: rows < 0, cols not a positive multiple of
+ * 32, an unknown act.
+ * --------------------------------------------------------------------------------- */
+int moe_activation_backward(int64_t rows, int32_t cols, const int32_t* live_rows, int act,
+                            const void* dy, const uint8_t* z_codes, const uint8_t* z_scales,
+                            void* dz, void* a, void* stream);
 
 #ifdef __cplusplus
 }
