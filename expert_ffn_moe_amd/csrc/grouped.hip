@@ -7,26 +7,18 @@
 //   linear  z = x W + b,  y = act(z) + residual, z kept as E4M3 codes with UE8M0 scales
 //   dx      dx = (dz W^T) act'(z),  a = act(z)
 //   dw      dW = x^T dz,  db = sum of dz
-//
-// One 64 x 64 output tile per block of 4 wavefronts (32 x 32 each, 16x16x32 bf16 matrix
-// instructions), the reduction in steps of 32 through LDS.
 #include <algorithm>
 
 #include "act.h"
 #include "bf16.h"
+#include "grouped_tile.h"
 #include "moe_internal.h"
 #include "wave.h"
 
 namespace moe {
 namespace {
 
-typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
-typedef float f32x4_t __attribute__((ext_vector_type(4)));
-typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
-
-constexpr int kTile = 64;
-constexpr int kStep = 32;
-constexpr int kPad = 40;  // LDS row stride in elements: 80 bytes
+constexpr int kXcds = 8;
 
 struct GroupedArgs {
   const uint16_t* x;    // linear, dw: x; dx: dz
@@ -52,140 +44,391 @@ __device__ __forceinline__ void segment(const int32_t* offsets, int R, int e, in
 
 enum GroupedMode { kLinear = 0, kDx = 1, kDw = 2 };
 
-template <int MODE>
-__global__ __launch_bounds__(256) void grouped_kernel(const GroupedArgs g) {
-  __shared__ uint16_t As[kTile][kPad], Bs[kTile][kPad];
-  __shared__ float tile[kTile][kTile + 1];
-  __shared__ int s_e, s_row, s_hi;
-  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
-  const int cols = MODE == kDx ? g.K : g.N;
-  const int n0 = blockIdx.x * kTile;
-  int e, m0, m1, k1, lo, hi;  // output rows m0 .. m1, reduction 0 .. k1
-  if (MODE == kDw) {
-    e = blockIdx.z;
-    segment(g.offsets, g.R, e, lo, hi);
-    m0 = blockIdx.y * kTile;
-    m1 = g.K;
-    k1 = hi - lo;
-  } else {
-    if (tid == 0) {
-      int t = blockIdx.y;
-      s_e = -1;
-      for (int i = 0; i < g.E; ++i) {
-        segment(g.offsets, g.R, i, lo, hi);
-        const int nt = div_up(hi - lo, kTile);
-        if (t < nt) {
-          s_e = i;
-          s_row = lo + t * kTile;
-          s_hi = hi;
-          break;
-        }
-        t -= nt;
+// One output tile.
+struct Item {
+  int e;      // expert
+  int m0;     // linear, dx: first row; dw: first of K
+  int rows;   // live rows of the tile
+  int n0;     // first output column
+  int lo;     // dw: first row of the reduction
+  int red;    // length of the reduction
+};
+
+// Persistent: the blocks of an XCD (workgroups go to XCDs round-robin) take the items of its
+// contiguous share in turn, expert by expert, the M tiles of an N group next to each other, so
+// that the operand bytes the items share come from that XCD's L2.  The next item's first
+// stage is copied while the last one of the current item computes.
+template <int MODE, bool GATHER, int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2, 2)))
+void tile_kernel(const GroupedArgs g) {
+  constexpr int NT = 64 * WM * WN;
+  constexpr int FM = BM / 16 / WM, FN = BN / 16 / WN;  // fragments of a wavefront
+  constexpr int AMODE = MODE == kDw ? kCols : kRows, BMODE = MODE == kDx ? kRows : kCols;
+  using A = Operand<AMODE, BM, NT>;
+  using B = Operand<BMODE, BN, NT>;
+  constexpr int kSlot = A::kBytes + B::kBytes;
+  __shared__ __align__(1024) char smem[2 * kSlot];
+  __shared__ int s_start[kMaxE + 1];
+  __shared__ int s_wsum[WM * WN];
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave / WN, wn = wave % WN;
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(MOE_LDS char*)smem;
+  const int ncols = MODE == kDx ? g.K : g.N;
+  const int ntn = div_up(ncols, BN);
+
+  // ---- the items of this block's XCD
+  int lo_t, items;  // linear, dx: M tiles; dw: (expert, K tile) pairs
+  const int xcd = blockIdx.x % kXcds, slots = gridDim.x / kXcds;
+  {
+    int total;
+    if constexpr (MODE == kDw) {
+      total = g.E * div_up(g.K, BM);
+    } else {
+      const int per = div_up(g.E, NT);
+      const int e0 = min(g.E, tid * per), e1 = min(g.E, e0 + per);
+      int sum = 0, lo, hi;
+      for (int e = e0; e < e1; ++e) {
+        segment(g.offsets, g.R, e, lo, hi);
+        sum += div_up(hi - lo, BM);
       }
+      const int inc = wave_inclusive_scan(sum);
+      if (lane == 63) s_wsum[wave] = inc;
+      __syncthreads();
+      int base = inc - sum;
+      for (int w = 0; w < wave; ++w) base += s_wsum[w];
+      for (int e = e0; e < e1; ++e) {
+        segment(g.offsets, g.R, e, lo, hi);
+        s_start[e] = base;
+        base += div_up(hi - lo, BM);
+      }
+      if (tid == NT - 1) s_start[g.E] = base;
+      __syncthreads();
+      total = s_start[g.E];
     }
-    __syncthreads();
-    e = s_e;
-    if (e < 0) return;  // block-uniform
-    m0 = s_row;
-    m1 = s_hi;
-    lo = 0;
-    k1 = MODE == kLinear ? g.K : g.N;
+    lo_t = (int)((int64_t)total * xcd / kXcds);
+    items = ((int)((int64_t)total * (xcd + 1) / kXcds) - lo_t) * ntn;
   }
-  const size_t wbase = (size_t)e * g.K * g.N;
-  f32x4_t acc[2][2] = {};
-  for (int k0 = 0; k0 < k1; k0 += kStep) {
-    for (int i = tid; i < kTile * kStep; i += 256) {
-      uint16_t av = 0, bv = 0;
-      if (MODE == kDw) {  // both operands have the reduction as their row
-        const int c = i % kTile, k = i / kTile;
-        if (k0 + k < k1) {
-          const int r = lo + k0 + k;
-          const int xr = g.row_token ? g.row_token[r] : r;
-          const bool ok = !g.row_token || (unsigned)xr < (unsigned)g.T;
-          if (m0 + c < m1 && ok) av = g.x[(size_t)xr * g.K + m0 + c];
-          if (n0 + c < cols) bv = g.w[(size_t)r * g.N + n0 + c];
-        }
-        As[c][k] = av;
-        Bs[c][k] = bv;
-      } else {
-        const int k = i % kStep, c = i / kStep;
-        if (k0 + k < k1 && m0 + c < m1) {
-          const int r = m0 + c;
-          const int xr = g.row_token ? g.row_token[r] : r;
-          if (!g.row_token || (unsigned)xr < (unsigned)g.T) av = g.x[(size_t)xr * k1 + k0 + k];
-        }
-        As[c][k] = av;
-        if (MODE == kDx) {
-          if (k0 + k < k1 && n0 + c < cols) bv = g.w[wbase + (size_t)(n0 + c) * g.N + k0 + k];
-          Bs[c][k] = bv;
+  auto find = [&](int item) {
+    Item t;
+    if constexpr (MODE == kDw) {
+      const int ntk = div_up(g.K, BM), q = lo_t + item / ntn;
+      t.e = q / ntk;
+      t.m0 = (q - t.e * ntk) * BM;
+      t.rows = min(BM, g.K - t.m0);
+      t.n0 = (item % ntn) * BN;
+      int hi;
+      segment(g.offsets, g.R, t.e, t.lo, hi);
+      t.red = hi - t.lo;
+    } else {
+      const int hi_t = lo_t + items / ntn;
+      int lo = 0, hi = g.E;
+      const int q = lo_t + item / ntn;
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (s_start[mid] <= q) lo = mid; else hi = mid;
+      }
+      t.e = __builtin_amdgcn_readfirstlane(lo);
+      // the expert's items in this share: N group major, M tile minor
+      const int seg0 = max(s_start[t.e], lo_t), nte = min(s_start[t.e + 1], hi_t) - seg0;
+      const int local = item - ntn * (seg0 - lo_t);
+      const int nt = local / nte, mt = seg0 + (local - nt * nte) - s_start[t.e];
+      int beg, end;
+      segment(g.offsets, g.R, t.e, beg, end);
+      t.m0 = __builtin_amdgcn_readfirstlane(beg + mt * BM);
+      t.rows = __builtin_amdgcn_readfirstlane(min(BM, end - t.m0));
+      t.n0 = __builtin_amdgcn_readfirstlane(nt * BN);
+      t.lo = 0;
+      t.red = MODE == kLinear ? g.K : g.N;
+    }
+    return t;
+  };
+
+  // ---- copies
+  A a;
+  B b;
+  uint32_t a_step[A::kLoads];  // kRows with a gather: 0 pins a lane to the zeros
+  int tok[A::kLoads];          // kCols with a gather: the rows of the next stage to be copied
+  int tok_row = 0, tok_left = 0;
+  const char* const zeros = reinterpret_cast<const char*>(g_zeros);
+  const int a_ld = MODE == kDx ? g.N : g.K;  // row length of the A operand
+  auto load_tokens = [&]() {
+#pragma unroll
+    for (int i = 0; i < A::kLoads; ++i) {
+      const int r = A::row_of(tid, i);
+      tok[i] = r < tok_left ? g.row_token[tok_row + r] : -1;
+    }
+  };
+  auto setup = [&](const Item& t) {
+#pragma unroll
+    for (int i = 0; i < A::kLoads; ++i) {
+      const int r = A::row_of(tid, i), c = A::piece_of(tid, i) * 8;
+      if constexpr (AMODE == kRows) {
+        const int row = t.m0 + min(r, t.rows - 1);
+        if constexpr (GATHER) {
+          const int tk = g.row_token[row];
+          const bool ok = (unsigned)tk < (unsigned)g.T;
+          a.p[i] = ok ? (const char*)(g.x + (size_t)tk * a_ld + c) : zeros;
+          a_step[i] = ok ? 2 * kStage : 0;
         } else {
-          const int cn = i % kTile, kn = i / kTile;
-          if (k0 + kn < k1 && n0 + cn < cols) bv = g.w[wbase + (size_t)(k0 + kn) * g.N + n0 + cn];
-          Bs[cn][kn] = bv;
+          a.p[i] = (const char*)(g.x + (size_t)row * a_ld + c);
         }
+      } else {
+        const int col = min(t.m0 + c, g.K - 8);
+        a.p[i] = (const char*)(g.x + (GATHER ? (size_t)col : (size_t)(t.lo + r) * g.K + col));
       }
     }
-    __syncthreads();
-    // 16x16x32 operands: lane l holds row l % 16, reduction 8 (l / 16) .. + 8
-    bf16x8_t a[2], b[2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      a[i] = __builtin_bit_cast(
-          bf16x8_t, *(const u32x4*)&As[(wave >> 1) * 32 + 16 * i + (lane & 15)][8 * (lane >> 4)]);
-      b[i] = __builtin_bit_cast(
-          bf16x8_t, *(const u32x4*)&Bs[(wave & 1) * 32 + 16 * i + (lane & 15)][8 * (lane >> 4)]);
+    for (int i = 0; i < B::kLoads; ++i) {
+      const int r = B::row_of(tid, i), c = B::piece_of(tid, i) * 8;
+      if constexpr (MODE == kDx) {
+        const int row = min(t.n0 + r, g.K - 1);
+        b.p[i] = (const char*)(g.w + ((size_t)t.e * g.K + row) * g.N + c);
+      } else {
+        const size_t row = MODE == kLinear ? (size_t)t.e * g.K + r : (size_t)t.lo + r;
+        b.p[i] = (const char*)(g.w + row * g.N + min(t.n0 + c, g.N - 8));
+      }
+    }
+    if constexpr (MODE == kDw && GATHER) {
+      tok_row = t.lo;
+      tok_left = t.red;
+      load_tokens();
+    }
+  };
+  // One stage into a slot; left: what remains of the reduction (less than a stage: the rest of
+  // both operands reads as zeros).
+  auto issue = [&](int slot, int left, int rows) {
+    const uint32_t la = __builtin_amdgcn_readfirstlane(lds0 + slot * kSlot + wave * 1024);
+    const uint32_t lb = la + A::kBytes;
+#pragma unroll
+    for (int i = 0; i < A::kLoads; ++i) {
+      // rows behind the tile's last: their fragments are garbage and not stored
+      if (AMODE == kRows && i * A::kRowsPerLoad >= rows) break;
+      const char* src = a.p[i];
+      if constexpr (MODE == kDw && GATHER)
+        src = (unsigned)tok[i] < (unsigned)g.T ? src + (size_t)tok[i] * (2 * (size_t)g.K) : zeros;
+      if (left < kStage) {
+        const int at = AMODE == kRows ? A::piece_of(tid, i) * 8 : A::row_of(tid, i);
+        src = at < left ? src : zeros;
+      }
+      copy_to_lds(src, la + i * NT * 16);
+      if constexpr (AMODE == kRows)
+        a.p[i] += GATHER ? a_step[i] : 2 * kStage;
+      else if constexpr (!GATHER)
+        a.p[i] += 2 * kStage * (size_t)g.K;
     }
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < B::kLoads; ++i) {
+      const char* src = b.p[i];
+      if (left < kStage) {
+        const int at = BMODE == kRows ? B::piece_of(tid, i) * 8 : B::row_of(tid, i);
+        src = at < left ? src : zeros;
+      }
+      copy_to_lds(src, lb + i * NT * 16);
+      b.p[i] += BMODE == kRows ? 2 * kStage : 2 * kStage * (size_t)g.N;
+    }
+    if constexpr (MODE == kDw && GATHER) {
+      tok_row += kStage;
+      tok_left -= kStage;
+      load_tokens();
+    }
+  };
+
+  // ---- compute.  Fragment m of a wavefront is rows 16 (m WM + wm) ..: a tile with few live
+  // rows needs the same number of fragments in every wavefront.
+  uint32_t fa[AMODE == kRows ? 2 : FM], fb[BMODE == kRows ? 2 : FN];
+  if constexpr (AMODE == kRows) {
+    fa[0] = lds0 + rows_frag(lane, 0) + wm * 2048;
+    fa[1] = lds0 + rows_frag(lane, 1) + wm * 2048;
+  } else {
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
-        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[i], b[j], acc[i][j], 0, 0, 0);
-    __syncthreads();
+    for (int m = 0; m < FM; ++m) fa[m] = lds0 + cols_frag<BM>(lane, (m * WM + wm) * 16);
   }
-  // element i of lane l is row 4 (l / 16) + i, column l % 16
+  const int wcol = wn * FN * 16;
+  if constexpr (BMODE == kRows) {
+    fb[0] = lds0 + A::kBytes + rows_frag(lane, 0) + wcol * 128;
+    fb[1] = lds0 + A::kBytes + rows_frag(lane, 1) + wcol * 128;
+  } else {
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+    for (int n = 0; n < FN; ++n) fb[n] = lds0 + A::kBytes + cols_frag<BN>(lane, wcol + n * 16);
+  }
+  f32x4_t acc[FM][FN];
+  auto compute = [&](int slot, auto nm_c) {
+    constexpr int NM = decltype(nm_c)::value;
+    const uint32_t so = slot * kSlot;
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int kk = 0; kk < 2; ++kk) {
+      bf16x8_t av[NM], bv[FN];
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        tile[(wave >> 1) * 32 + 16 * i + 4 * (lane >> 4) + q][(wave & 1) * 32 + 16 * j +
-                                                              (lane & 15)] = acc[i][j][q];
-  __syncthreads();
-  // two threads per 32-column block of a row pair: thread = (row, block)
-  for (int i = tid; i < kTile * 2; i += 256) {
-    const int r = m0 + (i >> 1), c0 = n0 + (i & 1) * 32;
-    if (r >= m1 || c0 >= cols) continue;
-    const float* v = &tile[i >> 1][(i & 1) * 32];
-    const int nc = min(32, cols - c0);
-    const size_t o = (size_t)r * cols + c0;
-    if (MODE == kDw) {
-      float* d = g.dw + wbase + o;
-      for (int c = 0; c < nc; ++c) d[c] = g.accumulate ? d[c] + v[c] : v[c];
-    } else if (MODE == kDx) {
-      float z[4];
-      for (int c = 0; c < nc; ++c) {
-        float f = 0.0f, df = 1.0f;
-        if (g.codes) {
-          if (c % 4 == 0) unpack_ckpt4(*(const uint32_t*)(g.codes + o + c), g.scales[o / kQBlock], z);
-          act_both(g.act, z[c % 4], f, df);
-          if (g.a) g.a[o + c] = to_bf16(f);
+      for (int n = 0; n < FN; ++n)
+        bv[n] = BMODE == kRows ? read_rows(fb[kk] + so + n * 2048)
+                               : read_cols<BN>(fb[n] + so + kk * 64 * BN);
+#pragma unroll
+      for (int m = 0; m < NM; ++m)
+        av[m] = AMODE == kRows ? read_rows(fa[kk] + so + m * WM * 2048)
+                               : read_cols<BM>(fa[m] + so + kk * 64 * BM);
+#pragma unroll
+      for (int m = 0; m < NM; ++m)
+#pragma unroll
+        for (int n = 0; n < FN; ++n)
+          acc[m][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bv[n], av[m], acc[m][n], 0, 0, 0);
+    }
+  };
+
+  // ---- epilogue: the columns are the instruction's rows, so a lane holds 4 consecutive
+  // columns n0 + wcol + 16 n + 4 (lane / 16) .. + 3 of row lane % 16 of each fragment.
+  auto epilogue = [&](const Item& t, int nm) {
+    const int c4 = t.n0 + wcol + 4 * (lane >> 4);
+    if constexpr (MODE == kDw) {
+#pragma unroll
+      for (int m = 0; m < FM; ++m) {
+        const int r = (m * WM + wm) * 16 + (lane & 15);
+        if (r >= t.rows) continue;
+        float* o = g.dw + ((size_t)t.e * g.K + t.m0 + r) * g.N + c4;
+#pragma unroll
+        for (int n = 0; n < FN; ++n) {
+          if (c4 + 16 * n >= g.N) continue;
+          f32x4_t v = acc[m][n];
+          if (g.accumulate) v += *(const f32x4_t*)(o + 16 * n);
+          *(f32x4_t*)(o + 16 * n) = v;
         }
-        g.out[o + c] = to_bf16(v[c] * df);
       }
     } else {
-      float z[32], amax = 0.0f;
-      for (int c = 0; c < nc; ++c) {
-        z[c] = v[c] + (g.bias ? bf16_lo(g.bias[(size_t)e * cols + c0 + c]) : 0.0f);
-        amax = fmaxf(amax, amax_term(z[c]));
-        g.out[o + c] = to_bf16(act_value(g.act, z[c]) + (g.residual ? bf16_lo(g.residual[o + c]) : 0.0f));
+      static_assert(FN % 2 == 0, "pairs of fragments");
+      const int c8 = t.n0 + wcol + swapped_col(lane);  // after the exchange
+      uint2 bias[FN];
+#pragma unroll
+      for (int n = 0; n < FN; ++n) {
+        bias[n] = make_uint2(0, 0);
+        if (MODE == kLinear && g.bias && c4 + 16 * n < ncols)
+          bias[n] = *(const uint2*)(g.bias + (size_t)t.e * ncols + c4 + 16 * n);
       }
-      if (g.codes) {
-        const int ex = ue8m0_exp(amax);
-        g.scales[o / kQBlock] = (uint8_t)(ex + 127);
-        for (int c = 0; c < 32; c += 4) *(uint32_t*)(g.codes + o + c) = pack_fp8x4(z + c, -ex);
+#pragma unroll
+      for (int m = 0; m < FM; ++m) {
+        if (m >= nm) break;  // wave-uniform
+        const int r = (m * WM + wm) * 16 + (lane & 15);
+        const size_t row = (size_t)(t.m0 + r) * ncols;
+#pragma unroll
+        for (int n = 0; n < FN; n += 2) {
+          const int c = c8 + 16 * n;
+          const bool live = r < t.rows && c < ncols;
+          float v[8], y[8];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            v[i] = acc[m][n][i];
+            v[4 + i] = acc[m][n + 1][i];
+          }
+          if constexpr (MODE == kLinear) {
+            v[0] += bf16_lo(bias[n].x); v[1] += bf16_hi(bias[n].x);
+            v[2] += bf16_lo(bias[n].y); v[3] += bf16_hi(bias[n].y);
+            v[4] += bf16_lo(bias[n + 1].x); v[5] += bf16_hi(bias[n + 1].x);
+            v[6] += bf16_lo(bias[n + 1].y); v[7] += bf16_hi(bias[n + 1].y);
+            if (g.codes) {
+              // the fragment pair is one scale block of its row, spread over 4 lanes
+              float amax = 0.0f;
+#pragma unroll
+              for (int i = 0; i < 8; ++i) amax = fmaxf(amax, amax_term(v[i]));
+              const int ex = ue8m0_exp(max_groups(amax));
+              uint32_t q0 = pack_fp8x4(v, -ex), q1 = pack_fp8x4(v + 4, -ex);
+              swap16(q0, q1);
+              if (live) {
+                *(uint2*)(g.codes + row + c) = make_uint2(q0, q1);
+                if (lane < 16) g.scales[(row + c) / kQBlock] = (uint8_t)(ex + 127);
+              }
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y[i] = act_value(g.act, v[i]);
+            if (g.residual) {
+              uint4 q = make_uint4(0, 0, 0, 0);
+              if (live) q = *(const uint4*)(g.residual + row + c);
+              swap16(q.x, q.z);
+              swap16(q.y, q.w);
+              float f[8];
+              unpack8(q, f);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) y[i] += f[i];
+            }
+          } else {
+            if (g.codes) {
+              uint2 q = make_uint2(0, 0);
+              int sc = 127;
+              if (live) {
+                q = *(const uint2*)(g.codes + row + c);
+                sc = g.scales[(row + c) / kQBlock];
+              }
+              swap16(q.x, q.y);
+              float z[8], f[8];
+              unpack_ckpt4(q.x, sc, z);
+              unpack_ckpt4(q.y, sc, z + 4);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                float df;
+                act_both(g.act, z[i], f[i], df);
+                y[i] = v[i] * df;
+              }
+              if (g.a) {
+                uint4 o = pack8(f);
+                swap16(o.x, o.z);
+                swap16(o.y, o.w);
+                if (live) *(uint4*)(g.a + row + c) = o;
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) y[i] = v[i];
+            }
+          }
+          uint4 o = pack8(y);
+          swap16(o.x, o.z);
+          swap16(o.y, o.w);
+          if (live) *(uint4*)(g.out + row + c) = o;
+        }
       }
     }
+  };
+
+  int idx = blockIdx.x / kXcds;
+  if (idx >= items) return;  // block-uniform
+  Item cur = find(idx), nxt = cur;
+  setup(cur);
+  issue(0, cur.red, cur.rows);
+  wait_copies();
+  int slot = 0;
+  for (;;) {
+    const int nst = max(1, div_up(cur.red, kStage));
+    // fragments of this wavefront with live rows; none where all its columns are outside
+    const int nm = cur.n0 + wcol >= ncols ? 0 : min(FM, div_up(cur.rows - wm * 16, 16 * WM));
+    bool more = false;
+#pragma unroll
+    for (int m = 0; m < FM; ++m)
+#pragma unroll
+      for (int n = 0; n < FN; ++n) acc[m][n] = f32x4_t{};
+    for (int s = 0; s < nst; ++s) {
+      if (s > 0) wait_copies();
+      block_barrier();
+      if (s + 1 < nst) {
+        issue(slot ^ 1, cur.red - (s + 1) * kStage, cur.rows);
+      } else {
+        idx += slots;
+        more = idx < items;
+        if (more) {
+          nxt = find(idx);
+          setup(nxt);
+          issue(slot ^ 1, nxt.red, nxt.rows);
+        }
+      }
+      if (nm > FM / 2)
+        compute(slot, std::integral_constant<int, FM>{});
+      else if (nm > FM / 4)
+        compute(slot, std::integral_constant<int, FM / 2>{});
+      else if (nm > 0)
+        compute(slot, std::integral_constant<int, (FM >= 4 ? FM / 4 : 1)>{});
+      slot ^= 1;
+    }
+    wait_copies();  // the next item's first stage, before the stores join the count
+    if (nm > 0) epilogue(cur, nm);
+    if (!more) return;
+    cur = nxt;
   }
 }
 
@@ -225,6 +468,28 @@ __global__ __launch_bounds__(256) void act_backward_kernel(
   }
 }
 
+int cu_count() {
+  static const int n = [] {
+    int dev = 0, v = 0;
+    if (hipGetDevice(&dev) == hipSuccess &&
+        hipDeviceGetAttribute(&v, hipDeviceAttributeMultiprocessorCount, dev) == hipSuccess && v > 0)
+      return std::max(kXcds, v / kXcds * kXcds);
+    return 256;
+  }();
+  return n;
+}
+
+template <int MODE, bool GATHER>
+void launch_tiles(const GroupedArgs& g, hipStream_t s) {
+  const int rows = MODE == kDw ? g.K : g.R / g.E;
+  if (rows > 160)
+    hipLaunchKernelGGL((tile_kernel<MODE, GATHER, 256, 256, 2, 4>), dim3(cu_count()), dim3(512), 0,
+                       s, g);
+  else
+    hipLaunchKernelGGL((tile_kernel<MODE, GATHER, 128, 128, 2, 2>), dim3(2 * cu_count()),
+                       dim3(256), 0, s, g);
+}
+
 }  // namespace
 
 hipError_t launch_grouped_linear(const moe_grouped& p, const void* x, const int32_t* row_token,
@@ -234,8 +499,10 @@ hipError_t launch_grouped_linear(const moe_grouped& p, const void* x, const int3
   GroupedArgs g{(const uint16_t*)x, (const uint16_t*)w, row_token, offsets, (const uint16_t*)bias,
                 (const uint16_t*)residual, (uint16_t*)y, nullptr, codes, scales, nullptr, nullptr,
                 p.R, p.T, p.K, p.N, p.E, act, 0};
-  hipLaunchKernelGGL(grouped_kernel<kLinear>, dim3(div_up(p.N, kTile), div_up(p.R, kTile) + p.E),
-                     dim3(256), 0, s, g);
+  if (row_token)
+    launch_tiles<kLinear, true>(g, s);
+  else
+    launch_tiles<kLinear, false>(g, s);
   return hipGetLastError();
 }
 
@@ -245,8 +512,7 @@ hipError_t launch_grouped_dx(const moe_grouped& p, const void* dz, const int32_t
   GroupedArgs g{(const uint16_t*)dz, (const uint16_t*)w, nullptr, offsets, nullptr, nullptr,
                 (uint16_t*)dx, (uint16_t*)a, const_cast<uint8_t*>(codes),
                 const_cast<uint8_t*>(scales), nullptr, nullptr, p.R, p.T, p.K, p.N, p.E, act, 0};
-  hipLaunchKernelGGL(grouped_kernel<kDx>, dim3(div_up(p.K, kTile), div_up(p.R, kTile) + p.E),
-                     dim3(256), 0, s, g);
+  launch_tiles<kDx, false>(g, s);
   return hipGetLastError();
 }
 
@@ -256,8 +522,10 @@ hipError_t launch_grouped_dw(const moe_grouped& p, const void* x, const int32_t*
   GroupedArgs g{(const uint16_t*)x, (const uint16_t*)dz, row_token, offsets, nullptr, nullptr,
                 nullptr, nullptr, nullptr, nullptr, dw, dbias, p.R, p.T, p.K, p.N, p.E, 0,
                 accumulate};
-  hipLaunchKernelGGL(grouped_kernel<kDw>, dim3(div_up(p.N, kTile), div_up(p.K, kTile), p.E),
-                     dim3(256), 0, s, g);
+  if (row_token)
+    launch_tiles<kDw, true>(g, s);
+  else
+    launch_tiles<kDw, false>(g, s);
   if (dbias)
     hipLaunchKernelGGL(dbias_kernel, dim3(div_up(p.N, 64), p.E), dim3(64), 0, s, g);
   return hipGetLastError();
