@@ -145,50 +145,53 @@ void tile_kernel(const GroupedArgs g) {
     return t;
   };
 
-  // ---- copies
-  A a;
-  B b;
-  uint32_t a_step[A::kLoads];  // kRows with a gather: 0 pins a lane to the zeros
-  int tok[A::kLoads];          // kCols with a gather: the rows of the next stage to be copied
+  // ---- copies: each piece is base + 32-bit offset, the base moving on by a stage; gathered
+  // rows have an address of their own (linear) or are looked up stage by stage (dw)
+  uint32_t a_off[A::kLoads], b_off[B::kLoads];
+  const char *a_base, *b_base;
+  const char* a_ptr[MODE == kLinear && GATHER ? A::kLoads : 1];
+  int tok[MODE == kDw && GATHER ? A::kLoads : 1];  // rows of the next stage to be copied
   int tok_row = 0, tok_left = 0;
   const char* const zeros = reinterpret_cast<const char*>(g_zeros);
-  const int a_ld = MODE == kDx ? g.N : g.K;  // row length of the A operand
+  const size_t a_ld = 2 * (size_t)(MODE == kDx ? g.N : g.K);  // bytes of a row of A
+  const size_t b_ld = 2 * (size_t)g.N;
+  const size_t a_step = AMODE == kRows ? 2 * kStage : kStage * a_ld;
+  const size_t b_step = BMODE == kRows ? 2 * kStage : kStage * b_ld;
   auto load_tokens = [&]() {
 #pragma unroll
     for (int i = 0; i < A::kLoads; ++i) {
       const int r = A::row_of(tid, i);
-      tok[i] = r < tok_left ? g.row_token[tok_row + r] : -1;
+      tok[i] = r < tok_left ? g.row_token[tok_row + r] : 0;
     }
   };
-  auto setup = [&](const Item& t) {
+  auto setup = [&](const Item& t, int tid) {
+    a_base = (const char*)g.x + (AMODE == kRows ? (GATHER ? 0 : t.m0 * a_ld)
+                                                : (GATHER ? 0 : t.lo * a_ld) + 2 * (size_t)t.m0);
+    b_base = (const char*)g.w + (MODE == kLinear ? (size_t)t.e * g.K * b_ld + 2 * (size_t)t.n0
+                                 : MODE == kDx   ? ((size_t)t.e * g.K + t.n0) * b_ld
+                                                 : t.lo * b_ld + 2 * (size_t)t.n0);
 #pragma unroll
     for (int i = 0; i < A::kLoads; ++i) {
       const int r = A::row_of(tid, i), c = A::piece_of(tid, i) * 8;
-      if constexpr (AMODE == kRows) {
-        const int row = t.m0 + min(r, t.rows - 1);
+      if constexpr (AMODE == kRows) {  // rows behind the tile's last repeat it
+        const int row = min(r, t.rows - 1);
         if constexpr (GATHER) {
-          const int tk = g.row_token[row];
-          const bool ok = (unsigned)tk < (unsigned)g.T;
-          a.p[i] = ok ? (const char*)(g.x + (size_t)tk * a_ld + c) : zeros;
-          a_step[i] = ok ? 2 * kStage : 0;
+          // a token outside x reads row 0 here and zeros in the epilogue
+          const int tk = g.row_token[t.m0 + row];
+          a_ptr[i] = a_base + ((unsigned)tk < (unsigned)g.T ? tk : 0) * a_ld + 2 * c;
         } else {
-          a.p[i] = (const char*)(g.x + (size_t)row * a_ld + c);
+          a_off[i] = (uint32_t)(row * a_ld) + 2 * c;
         }
-      } else {
-        const int col = min(t.m0 + c, g.K - 8);
-        a.p[i] = (const char*)(g.x + (GATHER ? (size_t)col : (size_t)(t.lo + r) * g.K + col));
+      } else {  // columns behind the last repeat it
+        const int col = min(c, g.K - 8 - t.m0);
+        a_off[i] = (GATHER ? 0 : (uint32_t)(r * a_ld)) + 2 * col;
       }
     }
 #pragma unroll
     for (int i = 0; i < B::kLoads; ++i) {
       const int r = B::row_of(tid, i), c = B::piece_of(tid, i) * 8;
-      if constexpr (MODE == kDx) {
-        const int row = min(t.n0 + r, g.K - 1);
-        b.p[i] = (const char*)(g.w + ((size_t)t.e * g.K + row) * g.N + c);
-      } else {
-        const size_t row = MODE == kLinear ? (size_t)t.e * g.K + r : (size_t)t.lo + r;
-        b.p[i] = (const char*)(g.w + row * g.N + min(t.n0 + c, g.N - 8));
-      }
+      b_off[i] = BMODE == kRows ? (uint32_t)(min(r, ncols - 1 - t.n0) * b_ld) + 2 * c
+                                : (uint32_t)(r * b_ld) + 2 * min(c, ncols - 8 - t.n0);
     }
     if constexpr (MODE == kDw && GATHER) {
       tok_row = t.lo;
@@ -205,29 +208,35 @@ void tile_kernel(const GroupedArgs g) {
     for (int i = 0; i < A::kLoads; ++i) {
       // rows behind the tile's last: their fragments are garbage and not stored
       if (AMODE == kRows && i * A::kRowsPerLoad >= rows) break;
-      const char* src = a.p[i];
-      if constexpr (MODE == kDw && GATHER)
-        src = (unsigned)tok[i] < (unsigned)g.T ? src + (size_t)tok[i] * (2 * (size_t)g.K) : zeros;
-      if (left < kStage) {
-        const int at = AMODE == kRows ? A::piece_of(tid, i) * 8 : A::row_of(tid, i);
-        src = at < left ? src : zeros;
+      if (!GATHER && left >= kStage) {
+        copy_to_lds(a_base, a_off[i], la + i * NT * 16);
+      } else {
+        const char* src;
+        if constexpr (MODE == kLinear && GATHER)
+          src = a_ptr[i];
+        else if constexpr (MODE == kDw && GATHER)
+          src = (unsigned)tok[i] < (unsigned)g.T ? a_base + tok[i] * a_ld + a_off[i] : zeros;
+        else
+          src = a_base + a_off[i];
+        if (left < kStage) {
+          const int at = AMODE == kRows ? A::piece_of(tid, i) * 8 : A::row_of(tid, i);
+          src = at < left ? src : zeros;
+        }
+        copy_to_lds(src, la + i * NT * 16);
       }
-      copy_to_lds(src, la + i * NT * 16);
-      if constexpr (AMODE == kRows)
-        a.p[i] += GATHER ? a_step[i] : 2 * kStage;
-      else if constexpr (!GATHER)
-        a.p[i] += 2 * kStage * (size_t)g.K;
+      if constexpr (MODE == kLinear && GATHER) a_ptr[i] += a_step;
     }
 #pragma unroll
     for (int i = 0; i < B::kLoads; ++i) {
-      const char* src = b.p[i];
-      if (left < kStage) {
+      if (left >= kStage) {
+        copy_to_lds(b_base, b_off[i], lb + i * NT * 16);
+      } else {
         const int at = BMODE == kRows ? B::piece_of(tid, i) * 8 : B::row_of(tid, i);
-        src = at < left ? src : zeros;
+        copy_to_lds(at < left ? b_base + b_off[i] : zeros, lb + i * NT * 16);
       }
-      copy_to_lds(src, lb + i * NT * 16);
-      b.p[i] += BMODE == kRows ? 2 * kStage : 2 * kStage * (size_t)g.N;
     }
+    if (!GATHER) a_base += a_step;
+    b_base += b_step;
     if constexpr (MODE == kDw && GATHER) {
       tok_row += kStage;
       tok_left -= kStage;
@@ -256,10 +265,11 @@ void tile_kernel(const GroupedArgs g) {
   f32x4_t acc[FM][FN];
   auto compute = [&](int slot, auto nm_c) {
     constexpr int NM = decltype(nm_c)::value;
+    if constexpr (NM == 0) return;
     const uint32_t so = slot * kSlot;
 #pragma unroll
     for (int kk = 0; kk < 2; ++kk) {
-      bf16x8_t av[NM], bv[FN];
+      bf16x8_t av[NM > 0 ? NM : 1], bv[FN];
 #pragma unroll
       for (int n = 0; n < FN; ++n)
         bv[n] = BMODE == kRows ? read_rows(fb[kk] + so + n * 2048)
@@ -279,6 +289,10 @@ void tile_kernel(const GroupedArgs g) {
   // ---- epilogue: the columns are the instruction's rows, so a lane holds 4 consecutive
   // columns n0 + wcol + 16 n + 4 (lane / 16) .. + 3 of row lane % 16 of each fragment.
   auto epilogue = [&](const Item& t, int nm) {
+    // through an empty statement: otherwise what derives from the lane below is computed
+    // before the items' loop and kept in registers through it
+    int lane = threadIdx.x & 63;
+    asm volatile("" : "+v"(lane));
     const int c4 = t.n0 + wcol + 4 * (lane >> 4);
     if constexpr (MODE == kDw) {
 #pragma unroll
@@ -309,6 +323,9 @@ void tile_kernel(const GroupedArgs g) {
         if (m >= nm) break;  // wave-uniform
         const int r = (m * WM + wm) * 16 + (lane & 15);
         const size_t row = (size_t)(t.m0 + r) * ncols;
+        bool named = true;
+        if constexpr (GATHER)
+          named = (unsigned)g.row_token[t.m0 + min(r, t.rows - 1)] < (unsigned)g.T;
 #pragma unroll
         for (int n = 0; n < FN; n += 2) {
           const int c = c8 + 16 * n;
@@ -316,8 +333,8 @@ void tile_kernel(const GroupedArgs g) {
           float v[8], y[8];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            v[i] = acc[m][n][i];
-            v[4 + i] = acc[m][n + 1][i];
+            v[i] = named ? acc[m][n][i] : 0.0f;
+            v[4 + i] = named ? acc[m][n + 1][i] : 0.0f;
           }
           if constexpr (MODE == kLinear) {
             v[0] += bf16_lo(bias[n].x); v[1] += bf16_hi(bias[n].x);
@@ -390,7 +407,7 @@ void tile_kernel(const GroupedArgs g) {
   int idx = blockIdx.x / kXcds;
   if (idx >= items) return;  // block-uniform
   Item cur = find(idx), nxt = cur;
-  setup(cur);
+  setup(cur, tid);
   issue(0, cur.red, cur.rows);
   wait_copies();
   int slot = 0;
@@ -398,33 +415,46 @@ void tile_kernel(const GroupedArgs g) {
     const int nst = max(1, div_up(cur.red, kStage));
     // fragments of this wavefront with live rows; none where all its columns are outside
     const int nm = cur.n0 + wcol >= ncols ? 0 : min(FM, div_up(cur.rows - wm * 16, 16 * WM));
-    bool more = false;
 #pragma unroll
     for (int m = 0; m < FM; ++m)
 #pragma unroll
       for (int n = 0; n < FN; ++n) acc[m][n] = f32x4_t{};
-    for (int s = 0; s < nst; ++s) {
-      if (s > 0) wait_copies();
-      block_barrier();
-      if (s + 1 < nst) {
+    auto stages = [&](auto nm_c) {  // all but the last
+      for (int s = 0; s < nst - 1; ++s) {
+        if (s > 0) wait_copies();
+        block_barrier();
         issue(slot ^ 1, cur.red - (s + 1) * kStage, cur.rows);
-      } else {
-        idx += slots;
-        more = idx < items;
-        if (more) {
-          nxt = find(idx);
-          setup(nxt);
-          issue(slot ^ 1, nxt.red, nxt.rows);
-        }
+        compute(slot, nm_c);
+        slot ^= 1;
       }
-      if (nm > FM / 2)
-        compute(slot, std::integral_constant<int, FM>{});
-      else if (nm > FM / 4)
-        compute(slot, std::integral_constant<int, FM / 2>{});
-      else if (nm > 0)
-        compute(slot, std::integral_constant<int, (FM >= 4 ? FM / 4 : 1)>{});
-      slot ^= 1;
+    };
+    constexpr int kHalf = FM / 2, kQuarter = FM >= 4 ? FM / 4 : 1;
+    if (nm > kHalf)
+      stages(std::integral_constant<int, FM>{});
+    else if (nm > kQuarter)
+      stages(std::integral_constant<int, kHalf>{});
+    else if (nm > 0)
+      stages(std::integral_constant<int, kQuarter>{});
+    else
+      stages(std::integral_constant<int, 0>{});
+    if (nst > 1) wait_copies();
+    block_barrier();
+    idx += slots;
+    const bool more = idx < items;
+    if (more) {
+      int tid_v = tid;  // as in the epilogue
+      asm volatile("" : "+v"(tid_v));
+      nxt = find(idx);
+      setup(nxt, tid_v);
+      issue(slot ^ 1, nxt.red, nxt.rows);
     }
+    if (nm > kHalf)
+      compute(slot, std::integral_constant<int, FM>{});
+    else if (nm > kQuarter)
+      compute(slot, std::integral_constant<int, kHalf>{});
+    else if (nm > 0)
+      compute(slot, std::integral_constant<int, kQuarter>{});
+    slot ^= 1;
     wait_copies();  // the next item's first stage, before the stores join the count
     if (nm > 0) epilogue(cur, nm);
     if (!more) return;
@@ -432,16 +462,31 @@ void tile_kernel(const GroupedArgs g) {
   }
 }
 
-// db[e][n]: one thread per column, rows in order.
-__global__ __launch_bounds__(64) void dbias_kernel(const GroupedArgs g) {
-  const int e = blockIdx.y, n = blockIdx.x * 64 + threadIdx.x;
+// db[e][n]: a block per expert and 64 columns; 32 row lanes of 8 threads (8 columns each) take
+// the rows in turn and are added up in order.
+__global__ __launch_bounds__(256) void dbias_kernel(const GroupedArgs g) {
+  __shared__ float part[32][64 + 1];
+  const int e = blockIdx.y, c = threadIdx.x % 8 * 8, rl = threadIdx.x / 8;
+  const int n = blockIdx.x * 64 + c;
   int lo, hi;
   segment(g.offsets, g.R, e, lo, hi);
-  if (n >= g.N) return;
-  float s = 0.0f;
-  for (int r = lo; r < hi; ++r) s += bf16_lo(g.w[(size_t)r * g.N + n]);
-  float* d = g.dbias + (size_t)e * g.N + n;
-  *d = g.accumulate ? *d + s : s;
+  float s[8] = {};
+  if (n < g.N)
+    for (int r = lo + rl; r < hi; r += 32) {
+      float f[8];
+      unpack8(*(const uint4*)(g.w + (size_t)r * g.N + n), f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s[i] += f[i];
+    }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) part[rl][c + i] = s[i];
+  __syncthreads();
+  const int col = blockIdx.x * 64 + threadIdx.x;
+  if (threadIdx.x >= 64 || col >= g.N) return;
+  float v = 0.0f;
+  for (int r = 0; r < 32; ++r) v += part[r][threadIdx.x];
+  float* d = g.dbias + (size_t)e * g.N + col;
+  *d = g.accumulate ? *d + v : v;
 }
 
 // One 32-column block per thread.
@@ -527,7 +572,7 @@ hipError_t launch_grouped_dw(const moe_grouped& p, const void* x, const int32_t*
   else
     launch_tiles<kDw, false>(g, s);
   if (dbias)
-    hipLaunchKernelGGL(dbias_kernel, dim3(div_up(p.N, 64), p.E), dim3(64), 0, s, g);
+    hipLaunchKernelGGL(dbias_kernel, dim3(div_up(p.N, 64), p.E), dim3(256), 0, s, g);
   return hipGetLastError();
 }
 

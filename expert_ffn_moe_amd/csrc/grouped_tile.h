@@ -40,14 +40,25 @@ enum OperandMode { kRows = 0, kCols = 1 };
 // Source of the pieces outside an operand: 16 zero bytes, valid for every lane.
 __device__ __align__(16) const uint32_t g_zeros[4] = {0, 0, 0, 0};
 
-__device__ __forceinline__ void copy_to_lds(const void* src, uint32_t lds) {
-  // m0: the wavefront's LDS address (uniform); the wait state after writing it is required
+// 16 bytes per lane from base + off (base uniform), or from a lane's own address, to the
+// wavefront's 1 KiB at lds (uniform), lane by lane.  m0 carries the LDS address; one wait state
+// is required after writing it.
+__device__ __forceinline__ void copy_to_lds(const char* base, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
+               :
+               : "v"(off), "s"(base), "s"(lds)
+               : "memory");
+}
+__device__ __forceinline__ void copy_to_lds(const char* src, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off"
                :
                : "v"(src), "s"(lds)
                : "memory");
 }
-__device__ __forceinline__ void wait_copies() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+// Every copy of this wavefront has landed and every LDS read of it has returned.
+__device__ __forceinline__ void wait_copies() {
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+}
 __device__ __forceinline__ void block_barrier() {
   asm volatile("" ::: "memory");
   __builtin_amdgcn_s_barrier();
@@ -67,7 +78,6 @@ struct Operand {
   static constexpr int kLoads = C * 8 / NT;     // 16-byte pieces per thread and stage
   static constexpr int kPieces = MODE == kRows ? 8 : C / 8;  // per LDS row
   static constexpr int kRowsPerLoad = NT / kPieces;
-  const char* p[kLoads];
 
   // This thread's LDS row in load i and its piece of that row in the source.
   static __device__ __forceinline__ int row_of(int tid, int i) {

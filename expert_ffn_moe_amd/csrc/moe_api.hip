@@ -961,7 +961,7 @@ int moe_grouped_linear(const moe_grouped* g, const void* x, const int32_t* row_t
   int st = moe_grouped_check(g);
   if (st != MOE_OK) return st;
   if (!grouped_args_ok(*g, offsets, {x, w, bias, residual, y, z_codes}) || !w ||
-      (g->R > 0 && (!x || !y)) || !act_ok(act) || !z_codes != !z_scales)
+      (g->R > 0 && (!x || !y || (row_token && g->T < 1))) || !act_ok(act) || !z_codes != !z_scales)
     return MOE_ERR_INVALID_ARG;
   if (z_codes && g->N % kCkptBlock) return MOE_ERR_UNSUPPORTED;
   const size_t yb = rows_bf16(g->R, g->N);
@@ -1008,7 +1008,8 @@ int moe_grouped_linear_dw(const moe_grouped* g, const void* x, const int32_t* ro
                           float* dbias, void* ws, size_t ws_bytes, void* stream) {
   int st = moe_grouped_check(g);
   if (st != MOE_OK) return st;
-  if (!grouped_args_ok(*g, offsets, {x, dz, dw, dbias}) || !dw || (g->R > 0 && (!x || !dz)) ||
+  if (!grouped_args_ok(*g, offsets, {x, dz, dw, dbias}) || !dw ||
+      (g->R > 0 && (!x || !dz || (row_token && g->T < 1))) ||
       (accumulate != 0 && accumulate != 1))
     return MOE_ERR_INVALID_ARG;
   if (aliased({{dw, grouped_w(*g) * 4}, {dbias, (size_t)g->E * g->N * 4}, {ws, ws_bytes}},

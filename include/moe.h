@@ -454,7 +454,7 @@ int moe_layer_backward(const moe_problem* p, const void* x, const float* logits,
  *
  *   R     rows the row buffers hold (0: they may be NULL and nothing is enqueued, except that
  *         moe_grouped_linear_dw still clears its outputs)
- *   T     rows of x when they are read through row_token (ignored without row_token)
+ *   T     rows of x when they are read through row_token (then at least 1; ignored without)
  *   K, N  input and output width: multiples of 8
  *   E     experts, at most 1024
  * --------------------------------------------------------------------------------- */

@@ -57,6 +57,7 @@ def test_linear_refusals():
                dict(y=x), dict(y=w), dict(y=res), dict(y=zc), dict(zc=x), dict(zs=off),
                dict(y=ctypes.c_void_p(rt.value))):
         assert go(**kw) == inv, kw
+    assert go(p=m.GroupedProblem(64, 128, 96, 4, 0)) == inv  # rows of no tokens
     assert go(p=m.GroupedProblem(64, 128, 72, 4, 32)) == uns  # a checkpoint of 72 columns
     assert go(p=m.GroupedProblem(64, 12, 96, 4, 32)) == uns
     # no rows: nothing to do, nothing enqueued
@@ -98,6 +99,7 @@ def test_dw_refusals():
                dict(off=None), dict(x=off8), dict(dz=off8), dict(dw=off8), dict(db=off8),
                dict(dw=x), dict(db=dz), dict(db=dw), dict(dw=rt)):
         assert go(**kw) == inv, kw
+    assert go(p=m.GroupedProblem(64, 96, 128, 4, 0)) == inv  # rows of no tokens
 
 
 def test_activation_backward_refusals():
