@@ -19,6 +19,7 @@ namespace moe {
 namespace {
 
 constexpr int kXcds = 8;
+#define MOE_INLINE __attribute__((always_inline))
 
 struct GroupedArgs {
   const uint16_t* x;    // linear, dw: x; dx: dz
@@ -63,6 +64,7 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2,
 void tile_kernel(const GroupedArgs g) {
   constexpr int NT = 64 * WM * WN;
   constexpr int FM = BM / 16 / WM, FN = BN / 16 / WN;  // fragments of a wavefront
+  static_assert(FM % 4 == 0 && FN % 2 == 0, "tiles cut to a half and a quarter, column pairs");
   constexpr int AMODE = MODE == kDw ? kCols : kRows, BMODE = MODE == kDx ? kRows : kCols;
   using A = Operand<AMODE, BM, NT>;
   using B = Operand<BMODE, BN, NT>;
@@ -105,12 +107,12 @@ void tile_kernel(const GroupedArgs g) {
       }
       if (tid == NT - 1) s_start[g.E] = base;
       __syncthreads();
-      total = s_start[g.E];
+      total = __builtin_amdgcn_readfirstlane(s_start[g.E]);
     }
     lo_t = (int)((int64_t)total * xcd / kXcds);
     items = ((int)((int64_t)total * (xcd + 1) / kXcds) - lo_t) * ntn;
   }
-  auto find = [&](int item) {
+  auto find = [&](int item) MOE_INLINE {
     Item t;
     if constexpr (MODE == kDw) {
       const int ntk = div_up(g.K, BM), q = lo_t + item / ntn;
@@ -120,25 +122,27 @@ void tile_kernel(const GroupedArgs g) {
       t.n0 = (item % ntn) * BN;
       int hi;
       segment(g.offsets, g.R, t.e, t.lo, hi);
-      t.red = hi - t.lo;
+      t.lo = __builtin_amdgcn_readfirstlane(t.lo);
+      t.red = __builtin_amdgcn_readfirstlane(hi) - t.lo;
     } else {
       const int hi_t = lo_t + items / ntn;
+      auto start = [&](int e) MOE_INLINE { return __builtin_amdgcn_readfirstlane(s_start[e]); };
       int lo = 0, hi = g.E;
       const int q = lo_t + item / ntn;
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (s_start[mid] <= q) lo = mid; else hi = mid;
+        if (start(mid) <= q) lo = mid; else hi = mid;
       }
-      t.e = __builtin_amdgcn_readfirstlane(lo);
+      t.e = lo;
       // the expert's items in this share: N group major, M tile minor
-      const int seg0 = max(s_start[t.e], lo_t), nte = min(s_start[t.e + 1], hi_t) - seg0;
+      const int first = start(lo), seg0 = max(first, lo_t), nte = min(start(lo + 1), hi_t) - seg0;
       const int local = item - ntn * (seg0 - lo_t);
-      const int nt = local / nte, mt = seg0 + (local - nt * nte) - s_start[t.e];
+      const int nt = local / nte, mt = seg0 + (local - nt * nte) - first;
       int beg, end;
-      segment(g.offsets, g.R, t.e, beg, end);
+      segment(g.offsets, g.R, lo, beg, end);
       t.m0 = __builtin_amdgcn_readfirstlane(beg + mt * BM);
       t.rows = __builtin_amdgcn_readfirstlane(min(BM, end - t.m0));
-      t.n0 = __builtin_amdgcn_readfirstlane(nt * BN);
+      t.n0 = nt * BN;
       t.lo = 0;
       t.red = MODE == kLinear ? g.K : g.N;
     }
@@ -157,14 +161,14 @@ void tile_kernel(const GroupedArgs g) {
   const size_t b_ld = 2 * (size_t)g.N;
   const size_t a_step = AMODE == kRows ? 2 * kStage : kStage * a_ld;
   const size_t b_step = BMODE == kRows ? 2 * kStage : kStage * b_ld;
-  auto load_tokens = [&]() {
+  auto load_tokens = [&]() MOE_INLINE {
 #pragma unroll
     for (int i = 0; i < A::kLoads; ++i) {
       const int r = A::row_of(tid, i);
       tok[i] = r < tok_left ? g.row_token[tok_row + r] : 0;
     }
   };
-  auto setup = [&](const Item& t, int tid) {
+  auto setup = [&](const Item& t, int tid) MOE_INLINE {
     a_base = (const char*)g.x + (AMODE == kRows ? (GATHER ? 0 : t.m0 * a_ld)
                                                 : (GATHER ? 0 : t.lo * a_ld) + 2 * (size_t)t.m0);
     b_base = (const char*)g.w + (MODE == kLinear ? (size_t)t.e * g.K * b_ld + 2 * (size_t)t.n0
@@ -199,48 +203,98 @@ void tile_kernel(const GroupedArgs g) {
       load_tokens();
     }
   };
-  // One stage into a slot; left: what remains of the reduction (less than a stage: the rest of
-  // both operands reads as zeros).
-  auto issue = [&](int slot, int left, int rows) {
-    const uint32_t la = __builtin_amdgcn_readfirstlane(lds0 + slot * kSlot + wave * 1024);
-    const uint32_t lb = la + A::kBytes;
-#pragma unroll
-    for (int i = 0; i < A::kLoads; ++i) {
-      // rows behind the tile's last: their fragments are garbage and not stored
-      if (AMODE == kRows && i * A::kRowsPerLoad >= rows) break;
-      if (!GATHER && left >= kStage) {
-        copy_to_lds(a_base, a_off[i], la + i * NT * 16);
-      } else {
-        const char* src;
-        if constexpr (MODE == kLinear && GATHER)
-          src = a_ptr[i];
-        else if constexpr (MODE == kDw && GATHER)
-          src = (unsigned)tok[i] < (unsigned)g.T ? a_base + tok[i] * a_ld + a_off[i] : zeros;
-        else
-          src = a_base + a_off[i];
-        if (left < kStage) {
-          const int at = AMODE == kRows ? A::piece_of(tid, i) * 8 : A::row_of(tid, i);
-          src = at < left ? src : zeros;
-        }
-        copy_to_lds(src, la + i * NT * 16);
-      }
-      if constexpr (MODE == kLinear && GATHER) a_ptr[i] += a_step;
+  // Piece i of a whole stage (A's loads, then B's) into the slot at LDS address la.
+  auto copy_piece = [&](uint32_t la, int i) MOE_INLINE {
+    if (i >= A::kLoads) {
+      i -= A::kLoads;
+      copy_to_lds(b_base, b_off[i], la + A::kBytes + i * NT * 16);
+    } else if constexpr (MODE == kLinear && GATHER) {
+      copy_to_lds(a_ptr[i], la + i * NT * 16);
+      a_ptr[i] += a_step;
+    } else if constexpr (MODE == kDw && GATHER) {
+      const char* src = a_base + tok[i] * a_ld + a_off[i];
+      copy_to_lds((unsigned)tok[i] < (unsigned)g.T ? src : zeros, la + i * NT * 16);
+    } else {
+      copy_to_lds(a_base, a_off[i], la + i * NT * 16);
     }
-#pragma unroll
-    for (int i = 0; i < B::kLoads; ++i) {
-      if (left >= kStage) {
-        copy_to_lds(b_base, b_off[i], lb + i * NT * 16);
-      } else {
-        const int at = BMODE == kRows ? B::piece_of(tid, i) * 8 : B::row_of(tid, i);
-        copy_to_lds(at < left ? b_base + b_off[i] : zeros, lb + i * NT * 16);
-      }
+  };
+  // The last, partial stage of a reduction: what lies behind it reads as zeros.
+  auto copy_piece_tail = [&](uint32_t la, int i, int left, int tid) MOE_INLINE {
+    const char* src;
+    int at;
+    if (i >= A::kLoads) {
+      const int j = i - A::kLoads;
+      src = b_base + b_off[j];
+      at = BMODE == kRows ? B::piece_of(tid, j) * 8 : B::row_of(tid, j);
+      la += A::kBytes + j * NT * 16;
+    } else {
+      if constexpr (MODE == kLinear && GATHER)
+        src = a_ptr[i];
+      else if constexpr (MODE == kDw && GATHER)
+        src = (unsigned)tok[i] < (unsigned)g.T ? a_base + tok[i] * a_ld + a_off[i] : zeros;
+      else
+        src = a_base + a_off[i];
+      at = AMODE == kRows ? A::piece_of(tid, i) * 8 : A::row_of(tid, i);
+      la += i * NT * 16;
     }
-    if (!GATHER) a_base += a_step;
+    copy_to_lds(at < left ? src : zeros, la);
+  };
+  auto next_stage = [&]() MOE_INLINE {
+    if constexpr (!GATHER) a_base += a_step;
     b_base += b_step;
     if constexpr (MODE == kDw && GATHER) {
       tok_row += kStage;
       tok_left -= kStage;
       load_tokens();
+    }
+  };
+  auto slot_lds = [&](int slot) MOE_INLINE {
+    return (uint32_t)__builtin_amdgcn_readfirstlane(lds0 + slot * kSlot + wave * 1024);
+  };
+  // Loads of A that hold live rows when a tile's fragments are cut to nm of FM.
+  auto a_loads = [&](int nm) MOE_INLINE { return AMODE == kRows ? A::kLoads * nm / FM : A::kLoads; };
+
+  // The copies run two stages ahead of the arithmetic, through the items in order: the item
+  // being copied, what remains of its reduction (at least 1: an empty one is a stage of zeros),
+  // the live length of its partial stage and its fragment count.
+  int cp_idx = blockIdx.x / kXcds, cp_left = 0, cp_tail = 0, cp_nm = FM;
+  auto frags_of = [&](int rows) MOE_INLINE {  // fragments that are computed: FM, FM / 2 or FM / 4
+    return rows > BM / 2 ? FM : rows > BM / 4 ? FM / 2 : FM / 4;
+  };
+  auto begin_copies = [&]() MOE_INLINE {
+    int tid_v = tid;  // through an empty statement, see the epilogue
+    asm volatile("" : "+v"(tid_v));
+    const Item t = find(cp_idx);
+    setup(t, tid_v);
+    cp_left = max(t.red, 1);
+    cp_nm = frags_of(t.rows);
+    cp_tail = t.red % kStage;
+  };
+  auto copies_left = [&]() MOE_INLINE { return cp_idx < items; };  // block-uniform
+  auto copies_done = [&]() MOE_INLINE {  // a stage was copied
+    cp_left -= kStage;
+    if (cp_left > 0) next_stage();
+  };
+  // On to the next item where the last one's stages are all copied.
+  auto copies_next = [&]() MOE_INLINE {
+    if (cp_left > 0) return;
+    cp_idx += slots;
+    if (cp_idx < items) begin_copies();
+  };
+  // A stage of any kind into a slot.
+  auto copy_any = [&](int slot) MOE_INLINE {
+    const uint32_t la = slot_lds(slot);
+    const int na = a_loads(cp_nm);
+    if (cp_left >= kStage) {
+#pragma unroll
+      for (int i = 0; i < A::kLoads + B::kLoads; ++i)
+        if (i < na || i >= A::kLoads) copy_piece(la, i);
+    } else {
+      int tid_v = tid;
+      asm volatile("" : "+v"(tid_v));
+#pragma unroll
+      for (int i = 0; i < A::kLoads + B::kLoads; ++i)
+        if (i < na || i >= A::kLoads) copy_piece_tail(la, i, cp_tail, tid_v);
     }
   };
 
@@ -263,32 +317,66 @@ void tile_kernel(const GroupedArgs g) {
     for (int n = 0; n < FN; ++n) fb[n] = lds0 + A::kBytes + cols_frag<BN>(lane, wcol + n * 16);
   }
   f32x4_t acc[FM][FN];
-  auto compute = [&](int slot, auto nm_c) {
-    constexpr int NM = decltype(nm_c)::value;
-    if constexpr (NM == 0) return;
+  bf16x8_t a0[FM], a1[FM], b0[FN], b1[FN];  // the fragments of a stage's two halves
+  auto read_a = [&](uint32_t so, int kk, int m) MOE_INLINE {
+    return AMODE == kRows ? read_rows(fa[kk] + so + m * WM * 2048)
+                          : read_cols<BM>(fa[m] + so + kk * 64 * BM);
+  };
+  auto read_b = [&](uint32_t so, int kk, int n) MOE_INLINE {
+    return BMODE == kRows ? read_rows(fb[kk] + so + n * 2048)
+                          : read_cols<BN>(fb[n] + so + kk * 64 * BN);
+  };
+  auto mfma_row = [&](int m, const bf16x8_t& av, const bf16x8_t* bv) MOE_INLINE {
+#pragma unroll
+    for (int n = 0; n < FN; ++n)
+      acc[m][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bv[n], av, acc[m][n], 0, 0, 0);
+  };
+  // First half of a stage; the second half's fragments are read meanwhile, ahead of the last
+  // products, so that they are there when the wavefronts meet.
+  auto half0 = [&](int slot, auto nm_c) MOE_INLINE {
+    constexpr int NM = decltype(nm_c)::value, kReads = FN + NM;
     const uint32_t so = slot * kSlot;
 #pragma unroll
-    for (int kk = 0; kk < 2; ++kk) {
-      bf16x8_t av[NM > 0 ? NM : 1], bv[FN];
+    for (int m = 0; m < NM; ++m) {
+      constexpr int per = (kReads + NM - 1) / NM;
 #pragma unroll
-      for (int n = 0; n < FN; ++n)
-        bv[n] = BMODE == kRows ? read_rows(fb[kk] + so + n * 2048)
-                               : read_cols<BN>(fb[n] + so + kk * 64 * BN);
+      for (int q = m * per; q < (m + 1) * per && q < kReads; ++q) {
+        if (q < FN) b1[q] = read_b(so, 1, q);
+        else a1[q - FN] = read_a(so, 1, q - FN);
+      }
+      mfma_row(m, a0[m], b0);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  // Second half, with the copies of a whole stage into the slot just read (copy_c) and the first
+  // half's fragments of the next stage between the products (an item's last stage reads what
+  // the next item reads again).
+  auto half1 = [&](int slot, auto nm_c, auto copy_c) MOE_INLINE {
+    constexpr int NM = decltype(nm_c)::value;
+    constexpr int NA = AMODE == kRows ? A::kLoads * NM / FM : A::kLoads, NC = NA + B::kLoads;
+    const uint32_t so = (slot ^ 1) * kSlot;
+    const uint32_t la = slot_lds(slot);
 #pragma unroll
-      for (int m = 0; m < NM; ++m)
-        av[m] = AMODE == kRows ? read_rows(fa[kk] + so + m * WM * 2048)
-                               : read_cols<BM>(fa[m] + so + kk * 64 * BM);
+    for (int m = 0; m < NM; ++m) {
+      if constexpr (decltype(copy_c)::value) {
+        constexpr int per = (NC + NM - 1) / NM;
 #pragma unroll
-      for (int m = 0; m < NM; ++m)
+        for (int q = m * per; q < (m + 1) * per && q < NC; ++q)
+          copy_piece(la, q < NA ? q : q - NA + A::kLoads);
+      }
+      mfma_row(m, a1[m], b1);
+      if (m == 0) {
 #pragma unroll
-        for (int n = 0; n < FN; ++n)
-          acc[m][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bv[n], av[m], acc[m][n], 0, 0, 0);
+        for (int n = 0; n < FN; ++n) b0[n] = read_b(so, 0, n);
+      }
+      a0[m] = read_a(so, 0, m);
+      __builtin_amdgcn_sched_barrier(0);
     }
   };
 
   // ---- epilogue: the columns are the instruction's rows, so a lane holds 4 consecutive
   // columns n0 + wcol + 16 n + 4 (lane / 16) .. + 3 of row lane % 16 of each fragment.
-  auto epilogue = [&](const Item& t, int nm) {
+  auto epilogue = [&](const Item& t, int nm) MOE_INLINE {
     // through an empty statement: otherwise what derives from the lane below is computed
     // before the items' loop and kept in registers through it
     int lane = threadIdx.x & 63;
@@ -297,6 +385,7 @@ void tile_kernel(const GroupedArgs g) {
     if constexpr (MODE == kDw) {
 #pragma unroll
       for (int m = 0; m < FM; ++m) {
+        if (m >= nm) break;
         const int r = (m * WM + wm) * 16 + (lane & 15);
         if (r >= t.rows) continue;
         float* o = g.dw + ((size_t)t.e * g.K + t.m0 + r) * g.N + c4;
@@ -309,7 +398,6 @@ void tile_kernel(const GroupedArgs g) {
         }
       }
     } else {
-      static_assert(FN % 2 == 0, "pairs of fragments");
       const int c8 = t.n0 + wcol + swapped_col(lane);  // after the exchange
       uint2 bias[FN];
 #pragma unroll
@@ -320,7 +408,7 @@ void tile_kernel(const GroupedArgs g) {
       }
 #pragma unroll
       for (int m = 0; m < FM; ++m) {
-        if (m >= nm) break;  // wave-uniform
+        if (m >= nm) break;
         const int r = (m * WM + wm) * 16 + (lane & 15);
         const size_t row = (size_t)(t.m0 + r) * ncols;
         bool named = true;
@@ -406,59 +494,70 @@ void tile_kernel(const GroupedArgs g) {
 
   int idx = blockIdx.x / kXcds;
   if (idx >= items) return;  // block-uniform
-  Item cur = find(idx), nxt = cur;
-  setup(cur, tid);
-  issue(0, cur.red, cur.rows);
+  begin_copies();
+  copy_any(0);
+  copies_done();
+  copies_next();
+  if (copies_left()) {
+    copy_any(1);
+    copies_done();
+  }
   wait_copies();
+  block_barrier();
   int slot = 0;
-  for (;;) {
+  using Yes = std::true_type;
+  using No = std::false_type;
+  for (; idx < items; idx += slots) {
+    const Item cur = find(idx);
     const int nst = max(1, div_up(cur.red, kStage));
-    // fragments of this wavefront with live rows; none where all its columns are outside
-    const int nm = cur.n0 + wcol >= ncols ? 0 : min(FM, div_up(cur.rows - wm * 16, 16 * WM));
+    auto run = [&](auto nm_c) MOE_INLINE {
+      constexpr int NM = decltype(nm_c)::value;
 #pragma unroll
-    for (int m = 0; m < FM; ++m)
+      for (int m = 0; m < NM; ++m)
 #pragma unroll
-      for (int n = 0; n < FN; ++n) acc[m][n] = f32x4_t{};
-    auto stages = [&](auto nm_c) {  // all but the last
-      for (int s = 0; s < nst - 1; ++s) {
-        if (s > 0) wait_copies();
+        for (int n = 0; n < FN; ++n) acc[m][n] = f32x4_t{};
+#pragma unroll
+      for (int n = 0; n < FN; ++n) b0[n] = read_b(slot * kSlot, 0, n);
+#pragma unroll
+      for (int m = 0; m < NM; ++m) a0[m] = read_a(slot * kSlot, 0, m);
+      // Stages whose mid-point copies a whole stage of this same item: a loop without branches,
+      // which the register allocator needs (with one it kept two sets of accumulators).
+      const int fast = cp_idx == idx ? max(cp_left, 0) / kStage : 0;
+      int s = 0;
+      for (; s < fast; ++s) {
+        half0(slot, nm_c);
+        wait_copies();
         block_barrier();
-        issue(slot ^ 1, cur.red - (s + 1) * kStage, cur.rows);
-        compute(slot, nm_c);
+        half1(slot, nm_c, Yes{});
+        cp_left -= kStage;
+        next_stage();
         slot ^= 1;
       }
+      // The others: a partial stage, the next item's first ones, or nothing left to copy.
+      for (; s < nst; ++s) {
+        copies_next();
+        half0(slot, nm_c);
+        wait_copies();
+        block_barrier();
+        if (copies_left()) {
+          copy_any(slot);
+          copies_done();
+        }
+        half1(slot, nm_c, No{});
+        slot ^= 1;
+      }
+      if (cur.n0 + wcol < ncols) epilogue(cur, NM);
+      // a block of its own where the epilogue's lanes meet again: merged with the end of the
+      // loop, it would make the compiler take the loop's scalars for divergent
+      asm volatile("");
     };
-    constexpr int kHalf = FM / 2, kQuarter = FM >= 4 ? FM / 4 : 1;
-    if (nm > kHalf)
-      stages(std::integral_constant<int, FM>{});
-    else if (nm > kQuarter)
-      stages(std::integral_constant<int, kHalf>{});
-    else if (nm > 0)
-      stages(std::integral_constant<int, kQuarter>{});
+    const int nm = frags_of(cur.rows);
+    if (nm == FM)
+      run(std::integral_constant<int, FM>{});
+    else if (nm == FM / 2)
+      run(std::integral_constant<int, FM / 2>{});
     else
-      stages(std::integral_constant<int, 0>{});
-    if (nst > 1) wait_copies();
-    block_barrier();
-    idx += slots;
-    const bool more = idx < items;
-    if (more) {
-      int tid_v = tid;  // as in the epilogue
-      asm volatile("" : "+v"(tid_v));
-      nxt = find(idx);
-      setup(nxt, tid_v);
-      issue(slot ^ 1, nxt.red, nxt.rows);
-    }
-    if (nm > kHalf)
-      compute(slot, std::integral_constant<int, FM>{});
-    else if (nm > kQuarter)
-      compute(slot, std::integral_constant<int, kHalf>{});
-    else if (nm > 0)
-      compute(slot, std::integral_constant<int, kQuarter>{});
-    slot ^= 1;
-    wait_copies();  // the next item's first stage, before the stores join the count
-    if (nm > 0) epilogue(cur, nm);
-    if (!more) return;
-    cur = nxt;
+      run(std::integral_constant<int, FM / 4>{});
   }
 }
 
