@@ -1,4 +1,4 @@
-// The matrix-core tile of the grouped products: operands from their natural bf16 layouts,
+// What the kernels of the grouped products share: operands from their natural bf16 layouts,
 // copied to LDS by the load-to-LDS path and fed to 16x16x32 instructions.
 //
 // A stage is 64 of the reduction.  An operand whose reduction is contiguous in memory
@@ -13,7 +13,7 @@
 //   kRows  piece c of row r sits at c ^ f(r), f(r) = ((r >> 1) ^ (r << 2)) & 7: 16 rows at one
 //          c cover all 64 banks;
 //   kCols  piece c of row k sits at c ^ 2 ((k & 3) | (k >> 3 & m) << 2), m = 3 (256 columns) or
-//          1 (128): the 32-byte pairs that a transposing read takes from rows 8 g + 0 .. 3 of
+//          1 (128), for 64 columns 2 ((k >> 1 & 1) | (k >> 3 & 1) << 1): the 32-byte pairs that a transposing read takes from rows 8 g + 0 .. 3 of
 //          its four lane groups lie in different banks.
 //
 // The copies are written as inline assembly (they have no register outputs) with explicit
@@ -23,6 +23,10 @@
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
+
+#include "../../include/moe.h"
+#include "act.h"
+#include "bf16.h"
 
 namespace moe {
 
@@ -68,7 +72,9 @@ __device__ __forceinline__ void block_barrier() {
 __device__ __forceinline__ int rows_swizzle(int r) { return ((r >> 1) ^ (r << 2)) & 7; }
 template <int C>
 __device__ __forceinline__ int cols_swizzle(int k) {
-  return 2 * ((k & 3) | (((k >> 3) & (C >= 256 ? 3 : 1)) << 2));
+  static_assert(C == 64 || C == 128 || C == 256, "");
+  if (C == 64) return 2 * (((k >> 1) & 1) | (((k >> 3) & 1) << 1));  // two rows per 256 bytes
+  return 2 * ((k & 3) | (((k >> 3) & (C == 256 ? 3 : 1)) << 2));
 }
 
 // One operand of a tile: C rows (kRows) or columns (kCols), copied by NT threads.
@@ -101,12 +107,12 @@ __device__ __forceinline__ uint32_t cols_frag(int lane, int c0) {  // columns c0
   return k * C * 2 + ((c0 / 8) ^ cols_swizzle<C>(k)) * 16 + (lane & 3) * 8;
 }
 __device__ __forceinline__ bf16x8_t read_rows(uint32_t a) {
-  return __builtin_bit_cast(bf16x8_t, *(MOE_LDS const u32x4*)(a));
+  return __builtin_bit_cast(bf16x8_t, *(MOE_LDS const u32x4*)(uintptr_t)a);
 }
 template <int C>
 __device__ __forceinline__ bf16x8_t read_cols(uint32_t a) {
-  const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((MOE_LDS s16x4*)(a));
-  const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((MOE_LDS s16x4*)(a + 4 * C * 2));
+  const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((MOE_LDS s16x4*)(uintptr_t)a);
+  const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((MOE_LDS s16x4*)(uintptr_t)(a + 4 * C * 2));
   return __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
@@ -130,6 +136,101 @@ __device__ __forceinline__ float max_groups(float v) {
   const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(m), __float_as_uint(m), false,
                                                   false);
   return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+
+struct GroupedArgs {
+  const uint16_t* x;    // linear, dw: x; dx: dz
+  const uint16_t* w;    // linear, dx: W; dw: dz
+  const int32_t* row_token;
+  const int32_t* offsets;
+  const uint16_t* bias;
+  const uint16_t* residual;
+  uint16_t* out;
+  uint16_t* a;
+  uint8_t* codes;
+  uint8_t* scales;
+  float* dw;
+  float* dbias;
+  int R, T, K, N, E, act, accumulate;
+  int split;    // parts of the reduction; with more than one their sums go to `part`
+  float* part;  // linear, dx: [split][R][columns]; dw: [split][E][K][N]
+  int* claim;   // the tile kernels' item counters, or NULL
+};
+
+// Rows [lo, hi) of expert e, inside [0, R) whatever offsets holds.
+__device__ __forceinline__ void segment(const int32_t* offsets, int R, int e, int& lo, int& hi) {
+  lo = offsets ? min(max(offsets[e], 0), R) : 0;
+  hi = offsets ? max(lo, min(offsets[e + 1], R)) : R;
+}
+
+enum GroupedMode { kLinear = 0, kDx = 1, kDw = 2 };
+
+// Which kernel a call takes, chosen from its sizes alone (the row counts are on the device).
+enum GroupedKernel { kStream = 0, kTile256, kTile128, kTile64 };
+struct GroupedPlan {
+  GroupedKernel kernel;
+  int split;
+  bool claims;
+  size_t part_bytes, ws_bytes;
+};
+constexpr size_t kClaimBytes = 256;
+GroupedPlan grouped_plan(const moe_grouped& p, int mode);
+
+// ---- grouped_stream.hip: linear and dx for a few rows per expert
+constexpr int kStreamCols = 64;
+hipError_t launch_grouped_stream(const GroupedArgs& g, int mode, hipStream_t s);
+
+// Columns c .. c + 3 of row r of linear's or dx's output from its 4 sums v (a 32-column block:
+// 8 consecutive lanes, all of them here).
+template <int MODE>
+__device__ __forceinline__ void finish4(const GroupedArgs& g, int e, int r, int c, bool live,
+                                        f32x4_t v) {
+  const int ncols = MODE == kDx ? g.K : g.N;
+  const size_t o = (size_t)r * ncols + c;
+  float y[4];
+  if constexpr (MODE == kLinear) {
+    float z[4];
+    uint2 b = make_uint2(0, 0);
+    if (g.bias && live) b = *(const uint2*)(g.bias + (size_t)e * ncols + c);
+    z[0] = v[0] + bf16_lo(b.x);
+    z[1] = v[1] + bf16_hi(b.x);
+    z[2] = v[2] + bf16_lo(b.y);
+    z[3] = v[3] + bf16_hi(b.y);
+    if (g.codes) {  // uniform
+      float m = fmaxf(fmaxf(amax_term(z[0]), amax_term(z[1])),
+                      fmaxf(amax_term(z[2]), amax_term(z[3])));
+#pragma unroll
+      for (int d = 1; d < 8; d <<= 1) m = fmaxf(m, __shfl_xor(m, d, 64));
+      const int ex = ue8m0_exp(m);
+      if (live) {
+        *(uint32_t*)(g.codes + o) = pack_fp8x4(z, -ex);
+        if (c % kQBlock == 0) g.scales[o / kQBlock] = (uint8_t)(ex + 127);
+      }
+    }
+    uint2 q = make_uint2(0, 0);
+    if (g.residual && live) q = *(const uint2*)(g.residual + o);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] = act_value(g.act, z[i]);
+    y[0] += bf16_lo(q.x);
+    y[1] += bf16_hi(q.x);
+    y[2] += bf16_lo(q.y);
+    y[3] += bf16_hi(q.y);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] = v[i];
+    if (g.codes && live) {
+      float z[4], f[4];
+      unpack_ckpt4(*(const uint32_t*)(g.codes + o), g.scales[o / kQBlock], z);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float df;
+        act_both(g.act, z[i], f[i], df);
+        y[i] *= df;
+      }
+      if (g.a) *(uint2*)(g.a + o) = make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]));
+    }
+  }
+  if (live) *(uint2*)(g.out + o) = make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
 }
 
 }  // namespace moe

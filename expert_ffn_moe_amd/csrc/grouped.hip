@@ -9,9 +9,7 @@
 //   dw      dW = x^T dz,  db = sum of dz
 #include <algorithm>
 
-#include "act.h"
-#include "bf16.h"
-#include "grouped_tile.h"
+#include "grouped.h"
 #include "moe_internal.h"
 #include "wave.h"
 
@@ -21,44 +19,30 @@ namespace {
 constexpr int kXcds = 8;
 #define MOE_INLINE __attribute__((always_inline))
 
-struct GroupedArgs {
-  const uint16_t* x;    // linear, dw: x; dx: dz
-  const uint16_t* w;    // linear, dx: W; dw: dz
-  const int32_t* row_token;
-  const int32_t* offsets;
-  const uint16_t* bias;
-  const uint16_t* residual;
-  uint16_t* out;
-  uint16_t* a;
-  uint8_t* codes;
-  uint8_t* scales;
-  float* dw;
-  float* dbias;
-  int R, T, K, N, E, act, accumulate;
-};
-
-// Rows [lo, hi) of expert e, inside [0, R) whatever offsets holds.
-__device__ __forceinline__ void segment(const int32_t* offsets, int R, int e, int& lo, int& hi) {
-  lo = offsets ? min(max(offsets[e], 0), R) : 0;
-  hi = offsets ? max(lo, min(offsets[e + 1], R)) : R;
-}
-
-enum GroupedMode { kLinear = 0, kDx = 1, kDw = 2 };
-
-// One output tile.
+// One output tile, or one part of its reduction.
 struct Item {
-  int e;      // expert
-  int m0;     // linear, dx: first row; dw: first of K
-  int rows;   // live rows of the tile
-  int n0;     // first output column
-  int lo;     // dw: first row of the reduction
-  int red;    // length of the reduction
+  int e;     // expert
+  int m0;    // linear, dx: first row; dw: first of K
+  int rows;  // live rows of the tile
+  int n0;    // first output column
+  int part;  // of a split reduction
+  int k0;    // first of the reduction (dw: a row of the layout)
+  int red;   // length of the reduction
 };
 
-// Persistent: the blocks of an XCD (workgroups go to XCDs round-robin) take the items of its
-// contiguous share in turn, expert by expert, the M tiles of an N group next to each other, so
-// that the operand bytes the items share come from that XCD's L2.  The next item's first
-// stage is copied while the last one of the current item computes.
+// A basic block of its own where lanes meet again after a divergent branch: merged with a block
+// that joins the paths of the items' loop, it would make the compiler take that loop's
+// scalars for divergent.
+__device__ __forceinline__ void meet() { asm volatile(""); }
+
+// Persistent.  The items are ordered expert by expert, within an expert N group by N group
+// (and part by part of a split reduction) with the M tiles innermost, and cut into 8 shares,
+// one per XCD (workgroups go to XCDs round-robin): the blocks of an XCD take its items in
+// turn, so that the operand bytes that neighbouring items share come from that XCD's L2.
+// Without counters a block takes every n-th item of its share.  With them (`claim`: 8 ints,
+// zero at launch) its further items are claimed one by one, from its own share and then from
+// the others', so blocks that drew cheap items (an expert's last rows) take more of them: with
+// 512 +- 22 rows per expert the static deal ended a quarter later than the average block.
 template <int MODE, bool GATHER, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2, 2)))
 void tile_kernel(const GroupedArgs g) {
@@ -70,82 +54,91 @@ void tile_kernel(const GroupedArgs g) {
   using B = Operand<BMODE, BN, NT>;
   constexpr int kSlot = A::kBytes + B::kBytes;
   __shared__ __align__(1024) char smem[2 * kSlot];
-  __shared__ int s_start[kMaxE + 1];
+  __shared__ int s_start[kMaxE + 1];  // linear, dx: M tiles before each expert
   __shared__ int s_wsum[WM * WN];
+  __shared__ int s_item[4];  // items taken, by their number mod 4; -1: none is left
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / WN, wn = wave % WN;
   const uint32_t lds0 = (uint32_t)(uintptr_t)(MOE_LDS char*)smem;
   const int ncols = MODE == kDx ? g.K : g.N;
-  const int ntn = div_up(ncols, BN);
+  const int ntn = div_up(ncols, BN), per_tile = ntn * g.split;  // items per M tile
 
-  // ---- the items of this block's XCD
-  int lo_t, items;  // linear, dx: M tiles; dw: (expert, K tile) pairs
+  // ---- all items, and this XCD's share of them
   const int xcd = blockIdx.x % kXcds, slots = gridDim.x / kXcds;
-  {
-    int total;
-    if constexpr (MODE == kDw) {
-      total = g.E * div_up(g.K, BM);
-    } else {
-      const int per = div_up(g.E, NT);
-      const int e0 = min(g.E, tid * per), e1 = min(g.E, e0 + per);
-      int sum = 0, lo, hi;
-      for (int e = e0; e < e1; ++e) {
-        segment(g.offsets, g.R, e, lo, hi);
-        sum += div_up(hi - lo, BM);
-      }
-      const int inc = wave_inclusive_scan(sum);
-      if (lane == 63) s_wsum[wave] = inc;
-      __syncthreads();
-      int base = inc - sum;
-      for (int w = 0; w < wave; ++w) base += s_wsum[w];
-      for (int e = e0; e < e1; ++e) {
-        segment(g.offsets, g.R, e, lo, hi);
-        s_start[e] = base;
-        base += div_up(hi - lo, BM);
-      }
-      if (tid == NT - 1) s_start[g.E] = base;
-      __syncthreads();
-      total = __builtin_amdgcn_readfirstlane(s_start[g.E]);
+  int total;
+  if constexpr (MODE == kDw) {
+    total = g.E * div_up(g.K, BM) * per_tile;
+  } else {
+    const int per = div_up(g.E, NT);
+    const int e0 = min(g.E, tid * per), e1 = min(g.E, e0 + per);
+    int sum = 0, lo, hi;
+    for (int e = e0; e < e1; ++e) {
+      segment(g.offsets, g.R, e, lo, hi);
+      sum += div_up(hi - lo, BM);
     }
-    lo_t = (int)((int64_t)total * xcd / kXcds);
-    items = ((int)((int64_t)total * (xcd + 1) / kXcds) - lo_t) * ntn;
+    const int inc = wave_inclusive_scan(sum);
+    if (lane == 63) s_wsum[wave] = inc;
+    __syncthreads();
+    int base = inc - sum;
+    for (int w = 0; w < wave; ++w) base += s_wsum[w];
+    for (int e = e0; e < e1; ++e) {
+      segment(g.offsets, g.R, e, lo, hi);
+      s_start[e] = base;
+      base += div_up(hi - lo, BM);
+    }
+    if (tid == NT - 1) s_start[g.E] = base;
+    __syncthreads();
+    total = __builtin_amdgcn_readfirstlane(s_start[g.E]) * per_tile;
   }
+  auto share = [&](int q) MOE_INLINE { return (int)((int64_t)total * q / kXcds); };
   auto find = [&](int item) MOE_INLINE {
     Item t;
+    int nt, stages;
     if constexpr (MODE == kDw) {
-      const int ntk = div_up(g.K, BM), q = lo_t + item / ntn;
+      const int ntk = div_up(g.K, BM), q = item / per_tile;
       t.e = q / ntk;
       t.m0 = (q - t.e * ntk) * BM;
       t.rows = min(BM, g.K - t.m0);
-      t.n0 = (item % ntn) * BN;
-      int hi;
-      segment(g.offsets, g.R, t.e, t.lo, hi);
-      t.lo = __builtin_amdgcn_readfirstlane(t.lo);
-      t.red = __builtin_amdgcn_readfirstlane(hi) - t.lo;
+      nt = item - q * per_tile;
+      int lo, hi;
+      segment(g.offsets, g.R, t.e, lo, hi);
+      t.k0 = __builtin_amdgcn_readfirstlane(lo);
+      t.red = __builtin_amdgcn_readfirstlane(hi) - t.k0;
     } else {
-      const int hi_t = lo_t + items / ntn;
       auto start = [&](int e) MOE_INLINE { return __builtin_amdgcn_readfirstlane(s_start[e]); };
       int lo = 0, hi = g.E;
-      const int q = lo_t + item / ntn;
+      const int q = item / per_tile;
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (start(mid) <= q) lo = mid; else hi = mid;
       }
       t.e = lo;
-      // the expert's items in this share: N group major, M tile minor
-      const int first = start(lo), seg0 = max(first, lo_t), nte = min(start(lo + 1), hi_t) - seg0;
-      const int local = item - ntn * (seg0 - lo_t);
-      const int nt = local / nte, mt = seg0 + (local - nt * nte) - first;
+      const int first = start(lo), tiles = start(lo + 1) - first;
+      const int local = item - per_tile * first;
+      nt = local / tiles;
       int beg, end;
       segment(g.offsets, g.R, lo, beg, end);
-      t.m0 = __builtin_amdgcn_readfirstlane(beg + mt * BM);
+      t.m0 = __builtin_amdgcn_readfirstlane(beg + (local - nt * tiles) * BM);
       t.rows = __builtin_amdgcn_readfirstlane(min(BM, end - t.m0));
-      t.n0 = nt * BN;
-      t.lo = 0;
+      t.k0 = 0;
       t.red = MODE == kLinear ? g.K : g.N;
     }
+    t.part = nt / ntn;
+    t.n0 = (nt - t.part * ntn) * BN;
+    if (g.split > 1) {  // whole stages per part
+      stages = div_up(t.red, kStage);
+      const int b = (int)((int64_t)stages * t.part / g.split) * kStage;
+      t.red = min(t.red, (int)((int64_t)stages * (t.part + 1) / g.split) * kStage) - b;
+      t.k0 += b;
+    }
+    // (known to be uniform: the copies' base addresses have to be scalars)
+    t.e = __builtin_amdgcn_readfirstlane(t.e);
+    t.n0 = __builtin_amdgcn_readfirstlane(t.n0);
+    t.part = __builtin_amdgcn_readfirstlane(t.part);
+    t.k0 = __builtin_amdgcn_readfirstlane(t.k0);
+    t.red = __builtin_amdgcn_readfirstlane(t.red);
     return t;
   };
 
@@ -169,11 +162,16 @@ void tile_kernel(const GroupedArgs g) {
     }
   };
   auto setup = [&](const Item& t, int tid) MOE_INLINE {
-    a_base = (const char*)g.x + (AMODE == kRows ? (GATHER ? 0 : t.m0 * a_ld)
-                                                : (GATHER ? 0 : t.lo * a_ld) + 2 * (size_t)t.m0);
-    b_base = (const char*)g.w + (MODE == kLinear ? (size_t)t.e * g.K * b_ld + 2 * (size_t)t.n0
-                                 : MODE == kDx   ? ((size_t)t.e * g.K + t.n0) * b_ld
-                                                 : t.lo * b_ld + 2 * (size_t)t.n0);
+    if constexpr (AMODE == kRows)
+      a_base = (const char*)g.x + 2 * (size_t)t.k0 + (GATHER ? 0 : t.m0 * a_ld);
+    else
+      a_base = (const char*)g.x + 2 * (size_t)t.m0 + (GATHER ? 0 : t.k0 * a_ld);
+    if constexpr (MODE == kLinear)
+      b_base = (const char*)g.w + ((size_t)t.e * g.K + t.k0) * b_ld + 2 * (size_t)t.n0;
+    else if constexpr (MODE == kDx)
+      b_base = (const char*)g.w + ((size_t)t.e * g.K + t.n0) * b_ld + 2 * (size_t)t.k0;
+    else
+      b_base = (const char*)g.w + t.k0 * b_ld + 2 * (size_t)t.n0;
 #pragma unroll
     for (int i = 0; i < A::kLoads; ++i) {
       const int r = A::row_of(tid, i), c = A::piece_of(tid, i) * 8;
@@ -198,7 +196,7 @@ void tile_kernel(const GroupedArgs g) {
                                 : (uint32_t)(r * b_ld) + 2 * min(c, ncols - 8 - t.n0);
     }
     if constexpr (MODE == kDw && GATHER) {
-      tok_row = t.lo;
+      tok_row = t.k0;
       tok_left = t.red;
       load_tokens();
     }
@@ -252,16 +250,24 @@ void tile_kernel(const GroupedArgs g) {
     return (uint32_t)__builtin_amdgcn_readfirstlane(lds0 + slot * kSlot + wave * 1024);
   };
   // Loads of A that hold live rows when a tile's fragments are cut to nm of FM.
-  auto a_loads = [&](int nm) MOE_INLINE { return AMODE == kRows ? A::kLoads * nm / FM : A::kLoads; };
+  auto a_loads = [&](int nm) MOE_INLINE { return AMODE == kRows ? div_up(A::kLoads * nm, FM) : A::kLoads; };
 
-  // The copies run two stages ahead of the arithmetic, through the items in order: the item
-  // being copied, what remains of its reduction (at least 1: an empty one is a stage of zeros),
-  // the live length of its partial stage and its fragment count.
-  int cp_idx = blockIdx.x / kXcds, cp_left = 0, cp_tail = 0, cp_nm = FM;
+  // The copies run two stages ahead of the arithmetic, through the items in the order taken:
+  // the item being copied (its number and index), what remains of its reduction (at least 1:
+  // an empty one is a stage of zeros), the live length of its partial stage and its fragment
+  // count.  The item after it is claimed when its own copies begin, so that the counter's
+  // answer is there when it is needed.
+  int cp_seq = 0, cp_idx = share(xcd) + (int)blockIdx.x / kXcds, cp_left = 0, cp_tail = 0,
+      cp_nm = FM;
+  int claimed = 0;  // thread 0: of this XCD's share
   auto frags_of = [&](int rows) MOE_INLINE {  // fragments that are computed: FM, FM / 2 or FM / 4
     return rows > BM / 2 ? FM : rows > BM / 4 ? FM / 2 : FM / 4;
   };
   auto begin_copies = [&]() MOE_INLINE {
+    if (g.claim && tid == 0)
+      claimed = __hip_atomic_fetch_add(g.claim + xcd, 1, __ATOMIC_RELAXED,
+                                       __HIP_MEMORY_SCOPE_AGENT);
+    meet();
     int tid_v = tid;  // through an empty statement, see the epilogue
     asm volatile("" : "+v"(tid_v));
     const Item t = find(cp_idx);
@@ -270,16 +276,35 @@ void tile_kernel(const GroupedArgs g) {
     cp_nm = frags_of(t.rows);
     cp_tail = t.red % kStage;
   };
-  auto copies_left = [&]() MOE_INLINE { return cp_idx < items; };  // block-uniform
+  auto copies_left = [&]() MOE_INLINE { return cp_idx >= 0; };  // block-uniform
   auto copies_done = [&]() MOE_INLINE {  // a stage was copied
     cp_left -= kStage;
     if (cp_left > 0) next_stage();
   };
   // On to the next item where the last one's stages are all copied.
   auto copies_next = [&]() MOE_INLINE {
-    if (cp_left > 0) return;
-    cp_idx += slots;
-    if (cp_idx < items) begin_copies();
+    if (cp_left > 0 || cp_idx < 0) return;
+    ++cp_seq;
+    if (tid == 0) {
+      int next = -1;
+      if (!g.claim) {
+        if (cp_idx + slots < share(xcd + 1)) next = cp_idx + slots;
+      } else {
+        // its own share, then what is left of the others'
+        for (int q = 0; q < kXcds && next < 0; ++q) {
+          const int o = (xcd + q) % kXcds;
+          if (q > 0)
+            claimed = __hip_atomic_fetch_add(g.claim + o, 1, __ATOMIC_RELAXED,
+                                             __HIP_MEMORY_SCOPE_AGENT);
+          if (claimed < share(o + 1) - share(o) - slots) next = share(o) + slots + claimed;
+        }
+      }
+      s_item[cp_seq & 3] = next;
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    }
+    block_barrier();
+    cp_idx = __builtin_amdgcn_readfirstlane(s_item[cp_seq & 3]);
+    if (cp_idx >= 0) begin_copies();
   };
   // A stage of any kind into a slot.
   auto copy_any = [&](int slot) MOE_INLINE {
@@ -353,7 +378,7 @@ void tile_kernel(const GroupedArgs g) {
   // the next item reads again).
   auto half1 = [&](int slot, auto nm_c, auto copy_c) MOE_INLINE {
     constexpr int NM = decltype(nm_c)::value;
-    constexpr int NA = AMODE == kRows ? A::kLoads * NM / FM : A::kLoads, NC = NA + B::kLoads;
+    constexpr int NA = AMODE == kRows ? (A::kLoads * NM + FM - 1) / FM : A::kLoads, NC = NA + B::kLoads;
     const uint32_t so = (slot ^ 1) * kSlot;
     const uint32_t la = slot_lds(slot);
 #pragma unroll
@@ -382,22 +407,29 @@ void tile_kernel(const GroupedArgs g) {
     int lane = threadIdx.x & 63;
     asm volatile("" : "+v"(lane));
     const int c4 = t.n0 + wcol + 4 * (lane >> 4);
-    if constexpr (MODE == kDw) {
+    if (MODE == kDw || g.split > 1) {
+      // fp32: the weight gradients, or a part's sums for the joining kernel
+      const size_t row0 = MODE == kDw ? ((size_t)t.part * g.E + t.e) * g.K + t.m0
+                                      : (size_t)t.part * g.R + t.m0;
+      float* const base = (g.split > 1 ? g.part : g.dw) + row0 * ncols + c4;
+      const bool add = MODE == kDw && g.split == 1 && g.accumulate;
 #pragma unroll
       for (int m = 0; m < FM; ++m) {
         if (m >= nm) break;
         const int r = (m * WM + wm) * 16 + (lane & 15);
         if (r >= t.rows) continue;
-        float* o = g.dw + ((size_t)t.e * g.K + t.m0 + r) * g.N + c4;
+        float* o = base + (size_t)r * ncols;
 #pragma unroll
         for (int n = 0; n < FN; ++n) {
-          if (c4 + 16 * n >= g.N) continue;
+          if (c4 + 16 * n >= ncols) continue;
           f32x4_t v = acc[m][n];
-          if (g.accumulate) v += *(const f32x4_t*)(o + 16 * n);
+          if (add) v += *(const f32x4_t*)(o + 16 * n);
           *(f32x4_t*)(o + 16 * n) = v;
         }
       }
-    } else {
+      return;
+    }
+    if constexpr (MODE != kDw) {
       const int c8 = t.n0 + wcol + swapped_col(lane);  // after the exchange
       uint2 bias[FN];
 #pragma unroll
@@ -492,8 +524,9 @@ void tile_kernel(const GroupedArgs g) {
     }
   };
 
-  int idx = blockIdx.x / kXcds;
-  if (idx >= items) return;  // block-uniform
+  if (cp_idx >= share(xcd + 1)) return;  // block-uniform
+  if (tid == 0) s_item[0] = cp_idx;
+  meet();
   begin_copies();
   copy_any(0);
   copies_done();
@@ -507,7 +540,9 @@ void tile_kernel(const GroupedArgs g) {
   int slot = 0;
   using Yes = std::true_type;
   using No = std::false_type;
-  for (; idx < items; idx += slots) {
+  for (int seq = 0;; ++seq) {
+    const int idx = __builtin_amdgcn_readfirstlane(s_item[seq & 3]);
+    if (idx < 0) return;  // block-uniform
     const Item cur = find(idx);
     const int nst = max(1, div_up(cur.red, kStage));
     auto run = [&](auto nm_c) MOE_INLINE {
@@ -522,7 +557,7 @@ void tile_kernel(const GroupedArgs g) {
       for (int m = 0; m < NM; ++m) a0[m] = read_a(slot * kSlot, 0, m);
       // Stages whose mid-point copies a whole stage of this same item: a loop without branches,
       // which the register allocator needs (with one it kept two sets of accumulators).
-      const int fast = cp_idx == idx ? max(cp_left, 0) / kStage : 0;
+      const int fast = cp_seq == seq ? max(cp_left, 0) / kStage : 0;
       int s = 0;
       for (; s < fast; ++s) {
         half0(slot, nm_c);
@@ -547,9 +582,7 @@ void tile_kernel(const GroupedArgs g) {
         slot ^= 1;
       }
       if (cur.n0 + wcol < ncols) epilogue(cur, NM);
-      // a block of its own where the epilogue's lanes meet again: merged with the end of the
-      // loop, it would make the compiler take the loop's scalars for divergent
-      asm volatile("");
+      meet();
     };
     const int nm = frags_of(cur.rows);
     if (nm == FM)
@@ -612,6 +645,47 @@ __global__ __launch_bounds__(256) void act_backward_kernel(
   }
 }
 
+// Adds the parts of a split linear or dx in order and finishes: 4 columns per thread, a row's
+// 32-column blocks in 8 consecutive lanes.
+template <int MODE>
+__global__ __launch_bounds__(256) void join_kernel(const GroupedArgs g) {
+  const int ncols = MODE == kDx ? g.K : g.N, nq = div_up(ncols, 32) * 8;
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int r = (int)(i / nq), c = (int)(i % nq) * 4;
+  int lo, hi;
+  segment(g.offsets, g.R, 0, lo, hi);
+  const int first = lo;  // rows outside every expert are left alone
+  if (g.offsets) hi = min(max(g.offsets[g.E], 0), g.R);
+  const bool live = r >= first && r < hi && c < ncols;
+  f32x4_t v = {};
+  int e = 0;
+  if (live) {
+    const size_t o = (size_t)r * ncols + c, plane = (size_t)g.R * ncols;
+    for (int p = 0; p < g.split; ++p) v += *(const f32x4_t*)(g.part + p * plane + o);
+    if (MODE == kLinear && g.bias && g.offsets) {  // the expert of row r
+      int top = g.E;
+      while (top - e > 1) {
+        const int mid = (e + top) >> 1;
+        if (g.offsets[mid] <= r) e = mid; else top = mid;
+      }
+    }
+    if (MODE == kLinear && g.row_token && (unsigned)g.row_token[r] >= (unsigned)g.T) v = f32x4_t{};
+  }
+  finish4<MODE>(g, e, r, c, live, v);
+}
+
+// dw = the parts of a split weight gradient, added in order.
+__global__ __launch_bounds__(256) void join_dw_kernel(const GroupedArgs g, int64_t n4) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= n4) return;
+  f32x4_t* const o = (f32x4_t*)g.dw + i;
+  f32x4_t v = g.accumulate ? *o : f32x4_t{};
+  for (int p = 0; p < g.split; ++p) v += *((const f32x4_t*)g.part + p * n4 + i);
+  *o = v;
+}
+
+__global__ void zero_claims_kernel(int* claim) { claim[threadIdx.x] = 0; }
+
 int cu_count() {
   static const int n = [] {
     int dev = 0, v = 0;
@@ -624,56 +698,121 @@ int cu_count() {
 }
 
 template <int MODE, bool GATHER>
-void launch_tiles(const GroupedArgs& g, hipStream_t s) {
-  const int rows = MODE == kDw ? g.K : g.R / g.E;
-  if (rows > 160)
+void launch_tiles(const GroupedArgs& g, GroupedKernel kernel, hipStream_t s) {
+  if (kernel == kTile256)
     hipLaunchKernelGGL((tile_kernel<MODE, GATHER, 256, 256, 2, 4>), dim3(cu_count()), dim3(512), 0,
                        s, g);
-  else
+  else if (kernel == kTile128)
     hipLaunchKernelGGL((tile_kernel<MODE, GATHER, 128, 128, 2, 2>), dim3(2 * cu_count()),
                        dim3(256), 0, s, g);
+  else
+    hipLaunchKernelGGL((tile_kernel<MODE, GATHER, 64, 128, 1, 4>), dim3(3 * cu_count()), dim3(256),
+                       0, s, g);
+}
+
+hipError_t run_grouped(const moe_grouped& p, GroupedArgs g, int mode, void* ws, hipStream_t s) {
+  const GroupedPlan plan = grouped_plan(p, mode);
+  g.split = plan.split;
+  g.part = plan.split > 1 ? static_cast<float*>(ws) : nullptr;
+  if (plan.claims) {
+    g.claim = reinterpret_cast<int*>(static_cast<char*>(ws) + plan.part_bytes);
+    hipLaunchKernelGGL(zero_claims_kernel, dim3(1), dim3(kXcds), 0, s, g.claim);
+  }
+  if (plan.kernel == kStream) {
+    const hipError_t err = launch_grouped_stream(g, mode, s);
+    if (err != hipSuccess) return err;
+  } else if (mode == kLinear) {
+    if (g.row_token) launch_tiles<kLinear, true>(g, plan.kernel, s);
+    else launch_tiles<kLinear, false>(g, plan.kernel, s);
+  } else if (mode == kDx) {
+    launch_tiles<kDx, false>(g, plan.kernel, s);
+  } else {
+    if (g.row_token) launch_tiles<kDw, true>(g, plan.kernel, s);
+    else launch_tiles<kDw, false>(g, plan.kernel, s);
+  }
+  if (plan.split > 1) {
+    if (mode == kDw) {
+      const int64_t n4 = (int64_t)g.E * g.K * g.N / 4;
+      hipLaunchKernelGGL(join_dw_kernel, dim3((unsigned)div_up64(n4, 256)), dim3(256), 0, s, g, n4);
+    } else {
+      const int64_t n = (int64_t)g.R * div_up(mode == kDx ? g.K : g.N, 32) * 8;
+      const dim3 grid((unsigned)div_up64(n, 256));
+      if (mode == kLinear) hipLaunchKernelGGL(join_kernel<kLinear>, grid, dim3(256), 0, s, g);
+      else hipLaunchKernelGGL(join_kernel<kDx>, grid, dim3(256), 0, s, g);
+    }
+  }
+  return hipGetLastError();
 }
 
 }  // namespace
 
+GroupedPlan grouped_plan(const moe_grouped& p, int mode) {
+  GroupedPlan plan{kTile64, 1, false, 0, 0};
+  const int ncols = mode == kDx ? p.K : p.N, red = mode == kLinear ? p.K : mode == kDx ? p.N : p.R;
+  const int64_t active = std::min(p.E, std::max(p.R, 1)), rows = p.R / p.E;
+  auto tiles = [&](int bm, int bn) -> int64_t {
+    const int64_t mt = mode == kDw ? (int64_t)p.E * div_up(p.K, bm)
+                                   : std::max<int64_t>(active, p.R / bm + (p.E > 1 ? p.E / 2 : 1));
+    return mt * div_up(ncols, bn);
+  };
+  const int64_t sblocks = active * div_up(ncols, kStreamCols);
+  int64_t items;
+  if (mode != kDw && p.R <= 16 * (int64_t)p.E && sblocks <= 1536) {
+    plan.kernel = kStream;
+    // parts of at least 512 of the reduction, up to a block per CU
+    plan.split = (int)std::max<int64_t>(1, std::min<int64_t>(red / 512, 256 / sblocks));
+    items = 0;
+  } else {
+    if ((mode == kDw || rows > 448) && tiles(256, 256) >= 256)
+      plan.kernel = kTile256;
+    else if (tiles(128, 128) >= 256)
+      plan.kernel = kTile128;
+    const int slots = plan.kernel == kTile256 ? 256 : plan.kernel == kTile128 ? 512 : 768;
+    items = plan.kernel == kTile256 ? tiles(256, 256)
+            : plan.kernel == kTile128 ? tiles(128, 128) : tiles(64, 128);
+    const int64_t per_expert = mode == kDw ? red / p.E : red;
+    plan.split = (int)std::max<int64_t>(1, std::min<int64_t>(per_expert / 256, slots / 2 / std::max<int64_t>(items, 1)));
+    plan.claims = plan.split == 1 && items > 4 * slots;
+  }
+  if (plan.split > 1)
+    plan.part_bytes = align256((size_t)plan.split * 4 *
+                               (mode == kDw ? (size_t)p.E * p.K * p.N : (size_t)p.R * ncols));
+  plan.ws_bytes = plan.part_bytes + (plan.claims ? kClaimBytes : 0);
+  return plan;
+}
+
 hipError_t launch_grouped_linear(const moe_grouped& p, const void* x, const int32_t* row_token,
                                  const int32_t* offsets, const void* w, const void* bias, int act,
                                  const void* residual, void* y, uint8_t* codes, uint8_t* scales,
-                                 hipStream_t s) {
+                                 void* ws, hipStream_t s) {
   GroupedArgs g{(const uint16_t*)x, (const uint16_t*)w, row_token, offsets, (const uint16_t*)bias,
                 (const uint16_t*)residual, (uint16_t*)y, nullptr, codes, scales, nullptr, nullptr,
-                p.R, p.T, p.K, p.N, p.E, act, 0};
-  if (row_token)
-    launch_tiles<kLinear, true>(g, s);
-  else
-    launch_tiles<kLinear, false>(g, s);
-  return hipGetLastError();
+                p.R, p.T, p.K, p.N, p.E, act, 0, 1, nullptr, nullptr};
+  return run_grouped(p, g, kLinear, ws, s);
 }
 
 hipError_t launch_grouped_dx(const moe_grouped& p, const void* dz, const int32_t* offsets,
                              const void* w, int act, const uint8_t* codes, const uint8_t* scales,
-                             void* dx, void* a, hipStream_t s) {
+                             void* dx, void* a, void* ws, hipStream_t s) {
   GroupedArgs g{(const uint16_t*)dz, (const uint16_t*)w, nullptr, offsets, nullptr, nullptr,
                 (uint16_t*)dx, (uint16_t*)a, const_cast<uint8_t*>(codes),
-                const_cast<uint8_t*>(scales), nullptr, nullptr, p.R, p.T, p.K, p.N, p.E, act, 0};
-  launch_tiles<kDx, false>(g, s);
-  return hipGetLastError();
+                const_cast<uint8_t*>(scales), nullptr, nullptr, p.R, p.T, p.K, p.N, p.E, act, 0, 1,
+                nullptr, nullptr};
+  return run_grouped(p, g, kDx, ws, s);
 }
 
 hipError_t launch_grouped_dw(const moe_grouped& p, const void* x, const int32_t* row_token,
                              const void* dz, const int32_t* offsets, int accumulate, float* dw,
-                             float* dbias, hipStream_t s) {
+                             float* dbias, void* ws, hipStream_t s) {
   GroupedArgs g{(const uint16_t*)x, (const uint16_t*)dz, row_token, offsets, nullptr, nullptr,
                 nullptr, nullptr, nullptr, nullptr, dw, dbias, p.R, p.T, p.K, p.N, p.E, 0,
-                accumulate};
-  if (row_token)
-    launch_tiles<kDw, true>(g, s);
-  else
-    launch_tiles<kDw, false>(g, s);
+                accumulate, 1, nullptr, nullptr};
   if (dbias)
     hipLaunchKernelGGL(dbias_kernel, dim3(div_up(p.N, 64), p.E), dim3(256), 0, s, g);
-  return hipGetLastError();
+  return run_grouped(p, g, kDw, ws, s);
 }
+
+size_t grouped_ws_bytes(const moe_grouped& p, int op) { return grouped_plan(p, op).ws_bytes; }
 
 hipError_t launch_act_backward(int64_t rows, int cols, const int32_t* live, int act,
                                const void* dy, const uint8_t* codes, const uint8_t* scales,

@@ -422,7 +422,6 @@ bool grouped_args_ok(const moe_grouped& g, const int32_t* offsets,
     if (!aligned16(q)) return false;
   return true;
 }
-size_t grouped_ws_bytes(const moe_grouped& g, int op) { return 0; }
 int check_grouped_ws(const moe_grouped& g, int op, const void* ws, size_t ws_bytes) {
   const size_t need = grouped_ws_bytes(g, op);
   if (need == 0) return MOE_OK;
@@ -975,7 +974,7 @@ int moe_grouped_linear(const moe_grouped* g, const void* x, const int32_t* row_t
   hipError_t err = check_grouped_device(*g, offsets, row_token, as_stream(stream));
   if (err == hipSuccess)
     err = launch_grouped_linear(*g, x, row_token, offsets, w, bias, act, residual, y, z_codes,
-                                z_scales, as_stream(stream));
+                                z_scales, ws, as_stream(stream));
   return status_of(err);
 }
 
@@ -999,7 +998,8 @@ int moe_grouped_linear_dx(const moe_grouped* g, const void* dz, const int32_t* o
   if (g->R == 0) return MOE_OK;
   hipError_t err = check_grouped_device(*g, offsets, nullptr, as_stream(stream));
   if (err == hipSuccess)
-    err = launch_grouped_dx(*g, dz, offsets, w, act, z_codes, z_scales, dx, a, as_stream(stream));
+    err = launch_grouped_dx(*g, dz, offsets, w, act, z_codes, z_scales, dx, a, ws,
+                            as_stream(stream));
   return status_of(err);
 }
 
@@ -1019,7 +1019,7 @@ int moe_grouped_linear_dw(const moe_grouped* g, const void* x, const int32_t* ro
   if ((st = check_grouped_ws(*g, MOE_GROUPED_DW, ws, ws_bytes)) != MOE_OK) return st;
   hipError_t err = check_grouped_device(*g, offsets, row_token, as_stream(stream));
   if (err == hipSuccess)
-    err = launch_grouped_dw(*g, x, row_token, dz, offsets, accumulate, dw, dbias,
+    err = launch_grouped_dw(*g, x, row_token, dz, offsets, accumulate, dw, dbias, ws,
                             as_stream(stream));
   return status_of(err);
 }

@@ -189,13 +189,15 @@ hipError_t launch_down_fp8(const moe_problem& p, const uint8_t* aq, const uint8_
 hipError_t launch_grouped_linear(const moe_grouped& g, const void* x, const int32_t* row_token,
                                  const int32_t* offsets, const void* w, const void* bias, int act,
                                  const void* residual, void* y, uint8_t* codes, uint8_t* scales,
-                                 hipStream_t s);
+                                 void* ws, hipStream_t s);
 hipError_t launch_grouped_dx(const moe_grouped& g, const void* dz, const int32_t* offsets,
                              const void* w, int act, const uint8_t* codes, const uint8_t* scales,
-                             void* dx, void* a, hipStream_t s);
+                             void* dx, void* a, void* ws, hipStream_t s);
 hipError_t launch_grouped_dw(const moe_grouped& g, const void* x, const int32_t* row_token,
                              const void* dz, const int32_t* offsets, int accumulate, float* dw,
-                             float* dbias, hipStream_t s);
+                             float* dbias, void* ws, hipStream_t s);
+// Workspace of a moe_grouped_op.
+size_t grouped_ws_bytes(const moe_grouped& g, int op);
 hipError_t launch_act_backward(int64_t rows, int cols, const int32_t* live, int act,
                                const void* dy, const uint8_t* codes, const uint8_t* scales,
                                void* dz, void* a, hipStream_t s);
