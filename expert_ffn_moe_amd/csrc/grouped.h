@@ -59,9 +59,20 @@ __device__ __forceinline__ void copy_to_lds(const char* src, uint32_t lds) {
                : "v"(src), "s"(lds)
                : "memory");
 }
-// Every copy of this wavefront has landed and every LDS read of it has returned.
+// 4 bytes per lane, to the wavefront's 256 bytes at lds.
+__device__ __forceinline__ void copy4_to_lds(const void* src, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off"
+               :
+               : "v"(src), "s"(lds)
+               : "memory");
+}
+// Every copy of this wavefront has landed and every LDS read of it has returned: vmcnt(0)
+// lgkmcnt(0) as the builtin, which the compiler takes into account (told nothing, it waited
+// once more in the middle of the next copies for a register reloaded long before).
 __device__ __forceinline__ void wait_copies() {
-  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0x0070);
+  asm volatile("" ::: "memory");
 }
 __device__ __forceinline__ void block_barrier() {
   asm volatile("" ::: "memory");
@@ -84,6 +95,8 @@ struct Operand {
   static constexpr int kLoads = C * 8 / NT;     // 16-byte pieces per thread and stage
   static constexpr int kPieces = MODE == kRows ? 8 : C / 8;  // per LDS row
   static constexpr int kRowsPerLoad = NT / kPieces;
+  // kCols: loads i and i + kKinds take the same piece of rows kKinds * kRowsPerLoad apart
+  static constexpr int kKinds = MODE == kCols && C == 256 && kRowsPerLoad == 16 ? 2 : 1;
 
   // This thread's LDS row in load i and its piece of that row in the source.
   static __device__ __forceinline__ int row_of(int tid, int i) {
@@ -92,6 +105,28 @@ struct Operand {
   static __device__ __forceinline__ int piece_of(int tid, int i) {
     const int r = row_of(tid, i), pos = tid % kPieces;
     return pos ^ (MODE == kRows ? rows_swizzle(r) : cols_swizzle<C>(r));
+  }
+
+  // 32-bit source offsets from a uniform base, in few registers.  kRows: that of load 0 and
+  // the last live row's (rows behind it repeat it); kCols: one per kind of load (pieces behind
+  // the last column repeat the last ones).
+  uint32_t off[2];
+  __device__ __forceinline__ void set(int tid, uint32_t ld, int last) {
+    if constexpr (MODE == kRows) {
+      off[0] = (uint32_t)row_of(tid, 0) * ld + 16 * piece_of(tid, 0);
+      off[1] = (uint32_t)min(last, C - 1) * ld + 16 * piece_of(tid, 0);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kKinds; ++i)
+        off[i] = (uint32_t)row_of(tid, i) * ld + 16 * min(piece_of(tid, i), last);
+    }
+  }
+  __device__ __forceinline__ const char* base_of(const char* base, int i, size_t ld) const {
+    return MODE == kRows ? base : base + (size_t)(i / kKinds * kKinds * kRowsPerLoad) * ld;
+  }
+  __device__ __forceinline__ uint32_t off_of(int i, uint32_t ld) const {
+    return MODE == kRows ? min(off[0] + (uint32_t)(i * kRowsPerLoad) * ld, off[1])
+                         : off[i % kKinds];
   }
 };
 
@@ -154,7 +189,6 @@ struct GroupedArgs {
   int R, T, K, N, E, act, accumulate;
   int split;    // parts of the reduction; with more than one their sums go to `part`
   float* part;  // linear, dx: [split][R][columns]; dw: [split][E][K][N]
-  int* claim;   // the tile kernels' item counters, or NULL
 };
 
 // Rows [lo, hi) of expert e, inside [0, R) whatever offsets holds.
@@ -169,11 +203,9 @@ enum GroupedMode { kLinear = 0, kDx = 1, kDw = 2 };
 enum GroupedKernel { kStream = 0, kTile256, kTile128, kTile64 };
 struct GroupedPlan {
   GroupedKernel kernel;
-  int split;
-  bool claims;
-  size_t part_bytes, ws_bytes;
+  int split;        // parts of the reduction
+  size_t ws_bytes;  // their sums
 };
-constexpr size_t kClaimBytes = 256;
 GroupedPlan grouped_plan(const moe_grouped& p, int mode);
 
 // ---- grouped_stream.hip: linear and dx for a few rows per expert

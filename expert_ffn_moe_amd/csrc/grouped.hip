@@ -35,20 +35,17 @@ struct Item {
 // scalars for divergent.
 __device__ __forceinline__ void meet() { asm volatile(""); }
 
-// Persistent.  The items are ordered expert by expert, within an expert N group by N group
-// (and part by part of a split reduction) with the M tiles innermost, and cut into 8 shares,
-// one per XCD (workgroups go to XCDs round-robin): the blocks of an XCD take its items in
-// turn, so that the operand bytes that neighbouring items share come from that XCD's L2.
-// Without counters a block takes every n-th item of its share.  With them (`claim`: 8 ints,
-// zero at launch) its further items are claimed one by one, from its own share and then from
-// the others', so blocks that drew cheap items (an expert's last rows) take more of them: with
-// 512 +- 22 rows per expert the static deal ended a quarter later than the average block.
+// Persistent.  The items are ordered expert by expert, within an expert by groups of 8 M tiles,
+// within a group N tile by N tile (and part by part of a split reduction) with the M tiles
+// innermost, and cut into 8 shares, one per XCD (workgroups go to XCDs round-robin); a block
+// takes every n-th item of its XCD's share, so that the operand bytes that neighbouring items
+// share (8 x 4 tiles at a time of a dense product) come from that XCD's L2.
 template <int MODE, bool GATHER, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2, 2)))
 void tile_kernel(const GroupedArgs g) {
   constexpr int NT = 64 * WM * WN;
   constexpr int FM = BM / 16 / WM, FN = BN / 16 / WN;  // fragments of a wavefront
-  static_assert(FM % 4 == 0 && FN % 2 == 0, "tiles cut to a half and a quarter, column pairs");
+  static_assert(FM % 4 == 0 && FN % 2 == 0, "tiles cut to quarters, column pairs");
   constexpr int AMODE = MODE == kDw ? kCols : kRows, BMODE = MODE == kDx ? kRows : kCols;
   using A = Operand<AMODE, BM, NT>;
   using B = Operand<BMODE, BN, NT>;
@@ -56,7 +53,7 @@ void tile_kernel(const GroupedArgs g) {
   __shared__ __align__(1024) char smem[2 * kSlot];
   __shared__ int s_start[kMaxE + 1];  // linear, dx: M tiles before each expert
   __shared__ int s_wsum[WM * WN];
-  __shared__ int s_item[4];  // items taken, by their number mod 4; -1: none is left
+  __shared__ int s_tok[MODE == kDw && GATHER ? WM * WN * 128 : 1];
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -95,17 +92,11 @@ void tile_kernel(const GroupedArgs g) {
   auto share = [&](int q) MOE_INLINE { return (int)((int64_t)total * q / kXcds); };
   auto find = [&](int item) MOE_INLINE {
     Item t;
-    int nt, stages;
+    int tiles, local, beg, end;  // of the expert: M tiles, the item's place, the rows
     if constexpr (MODE == kDw) {
-      const int ntk = div_up(g.K, BM), q = item / per_tile;
-      t.e = q / ntk;
-      t.m0 = (q - t.e * ntk) * BM;
-      t.rows = min(BM, g.K - t.m0);
-      nt = item - q * per_tile;
-      int lo, hi;
-      segment(g.offsets, g.R, t.e, lo, hi);
-      t.k0 = __builtin_amdgcn_readfirstlane(lo);
-      t.red = __builtin_amdgcn_readfirstlane(hi) - t.k0;
+      tiles = div_up(g.K, BM);
+      t.e = item / (tiles * per_tile);
+      local = item - t.e * tiles * per_tile;
     } else {
       auto start = [&](int e) MOE_INLINE { return __builtin_amdgcn_readfirstlane(s_start[e]); };
       int lo = 0, hi = g.E;
@@ -115,20 +106,34 @@ void tile_kernel(const GroupedArgs g) {
         if (start(mid) <= q) lo = mid; else hi = mid;
       }
       t.e = lo;
-      const int first = start(lo), tiles = start(lo + 1) - first;
-      const int local = item - per_tile * first;
-      nt = local / tiles;
-      int beg, end;
-      segment(g.offsets, g.R, lo, beg, end);
-      t.m0 = __builtin_amdgcn_readfirstlane(beg + (local - nt * tiles) * BM);
-      t.rows = __builtin_amdgcn_readfirstlane(min(BM, end - t.m0));
+      tiles = start(lo + 1) - start(lo);
+      local = item - per_tile * start(lo);
+    }
+    segment(g.offsets, g.R, t.e, beg, end);
+    constexpr int kGroup = 8;
+    const int group = local / (kGroup * per_tile) * kGroup;
+    local -= group * per_tile;
+    const int in_group = min(kGroup, tiles - group), nt = local / in_group;
+    const int mt = group + local - nt * in_group;
+    if constexpr (MODE == kDw) {
+      t.m0 = mt * BM;
+      t.rows = min(BM, g.K - t.m0);
+      t.k0 = beg;
+      t.red = end - beg;
+    } else {
+      // an expert's tiles are of even height (in steps of a fragment per wavefront row): their
+      // items take the same time and move through the weights together (534 rows as 3 x 192
+      // instead of 256 + 256 + 22: the 7168 -> 2048 product 4.7 -> 4.1 ms)
+      const int height = div_up(div_up(end - beg, tiles), 16 * WM) * 16 * WM;
+      t.m0 = __builtin_amdgcn_readfirstlane(beg + mt * height);
+      t.rows = __builtin_amdgcn_readfirstlane(min(height, end - t.m0));
       t.k0 = 0;
       t.red = MODE == kLinear ? g.K : g.N;
     }
     t.part = nt / ntn;
     t.n0 = (nt - t.part * ntn) * BN;
     if (g.split > 1) {  // whole stages per part
-      stages = div_up(t.red, kStage);
+      const int stages = div_up(t.red, kStage);
       const int b = (int)((int64_t)stages * t.part / g.split) * kStage;
       t.red = min(t.red, (int)((int64_t)stages * (t.part + 1) / g.split) * kStage) - b;
       t.k0 += b;
@@ -144,22 +149,25 @@ void tile_kernel(const GroupedArgs g) {
 
   // ---- copies: each piece is base + 32-bit offset, the base moving on by a stage; gathered
   // rows have an address of their own (linear) or are looked up stage by stage (dw)
-  uint32_t a_off[A::kLoads], b_off[B::kLoads];
+  A a{};
+  B b{};
   const char *a_base, *b_base;
   const char* a_ptr[MODE == kLinear && GATHER ? A::kLoads : 1];
-  int tok[MODE == kDw && GATHER ? A::kLoads : 1];  // rows of the next stage to be copied
-  int tok_row = 0, tok_left = 0;
+  int tok_row = 0, tok_par = 0;  // dw: first row of the next stage to be copied, its list's place
   const char* const zeros = reinterpret_cast<const char*>(g_zeros);
   const size_t a_ld = 2 * (size_t)(MODE == kDx ? g.N : g.K);  // bytes of a row of A
   const size_t b_ld = 2 * (size_t)g.N;
   const size_t a_step = AMODE == kRows ? 2 * kStage : kStage * a_ld;
   const size_t b_step = BMODE == kRows ? 2 * kStage : kStage * b_ld;
+  // dw with a gather: the tokens of the next stage's rows, as a copy to a list of this
+  // wavefront's own (two take turns), so that no register waits for them
+  const uint32_t tok_lds = (uint32_t)(uintptr_t)(MOE_LDS int*)s_tok + wave * 512;
   auto load_tokens = [&]() MOE_INLINE {
-#pragma unroll
-    for (int i = 0; i < A::kLoads; ++i) {
-      const int r = A::row_of(tid, i);
-      tok[i] = r < tok_left ? g.row_token[tok_row + r] : 0;
-    }
+    copy4_to_lds(g.row_token + min(tok_row + (int)(threadIdx.x & 63), g.R - 1),
+                 __builtin_amdgcn_readfirstlane(tok_lds + tok_par * 256));
+  };
+  auto token = [&](int i, int tid) MOE_INLINE {
+    return *(MOE_LDS const int*)(uintptr_t)(tok_lds + tok_par * 256 + A::row_of(tid, i) * 4);
   };
   auto setup = [&](const Item& t, int tid) MOE_INLINE {
     if constexpr (AMODE == kRows)
@@ -172,32 +180,20 @@ void tile_kernel(const GroupedArgs g) {
       b_base = (const char*)g.w + ((size_t)t.e * g.K + t.n0) * b_ld + 2 * (size_t)t.k0;
     else
       b_base = (const char*)g.w + t.k0 * b_ld + 2 * (size_t)t.n0;
+    if constexpr (MODE == kLinear && GATHER) {
+      // a token outside x reads row 0 here and zeros in the epilogue
 #pragma unroll
-    for (int i = 0; i < A::kLoads; ++i) {
-      const int r = A::row_of(tid, i), c = A::piece_of(tid, i) * 8;
-      if constexpr (AMODE == kRows) {  // rows behind the tile's last repeat it
-        const int row = min(r, t.rows - 1);
-        if constexpr (GATHER) {
-          // a token outside x reads row 0 here and zeros in the epilogue
-          const int tk = g.row_token[t.m0 + row];
-          a_ptr[i] = a_base + ((unsigned)tk < (unsigned)g.T ? tk : 0) * a_ld + 2 * c;
-        } else {
-          a_off[i] = (uint32_t)(row * a_ld) + 2 * c;
-        }
-      } else {  // columns behind the last repeat it
-        const int col = min(c, g.K - 8 - t.m0);
-        a_off[i] = (GATHER ? 0 : (uint32_t)(r * a_ld)) + 2 * col;
+      for (int i = 0; i < A::kLoads; ++i) {
+        const int tk = g.row_token[t.m0 + min(A::row_of(tid, i), t.rows - 1)];
+        a_ptr[i] = a_base + ((unsigned)tk < (unsigned)g.T ? tk : 0) * a_ld + 16 * A::piece_of(tid, i);
       }
+    } else {
+      a.set(tid, MODE == kDw && GATHER ? 0 : (uint32_t)a_ld,
+            AMODE == kRows ? t.rows - 1 : (g.K - t.m0) / 8 - 1);
     }
-#pragma unroll
-    for (int i = 0; i < B::kLoads; ++i) {
-      const int r = B::row_of(tid, i), c = B::piece_of(tid, i) * 8;
-      b_off[i] = BMODE == kRows ? (uint32_t)(min(r, ncols - 1 - t.n0) * b_ld) + 2 * c
-                                : (uint32_t)(r * b_ld) + 2 * min(c, ncols - 8 - t.n0);
-    }
+    b.set(tid, (uint32_t)b_ld, BMODE == kRows ? ncols - 1 - t.n0 : (ncols - t.n0) / 8 - 1);
     if constexpr (MODE == kDw && GATHER) {
       tok_row = t.k0;
-      tok_left = t.red;
       load_tokens();
     }
   };
@@ -205,15 +201,17 @@ void tile_kernel(const GroupedArgs g) {
   auto copy_piece = [&](uint32_t la, int i) MOE_INLINE {
     if (i >= A::kLoads) {
       i -= A::kLoads;
-      copy_to_lds(b_base, b_off[i], la + A::kBytes + i * NT * 16);
+      copy_to_lds(b.base_of(b_base, i, b_ld), b.off_of(i, (uint32_t)b_ld),
+                  la + A::kBytes + i * NT * 16);
     } else if constexpr (MODE == kLinear && GATHER) {
       copy_to_lds(a_ptr[i], la + i * NT * 16);
       a_ptr[i] += a_step;
     } else if constexpr (MODE == kDw && GATHER) {
-      const char* src = a_base + tok[i] * a_ld + a_off[i];
-      copy_to_lds((unsigned)tok[i] < (unsigned)g.T ? src : zeros, la + i * NT * 16);
+      const int tk = token(i, tid);
+      copy_to_lds((unsigned)tk < (unsigned)g.T ? a_base + tk * a_ld + a.off[i % A::kKinds] : zeros,
+                  la + i * NT * 16);
     } else {
-      copy_to_lds(a_base, a_off[i], la + i * NT * 16);
+      copy_to_lds(a.base_of(a_base, i, a_ld), a.off_of(i, (uint32_t)a_ld), la + i * NT * 16);
     }
   };
   // The last, partial stage of a reduction: what lies behind it reads as zeros.
@@ -222,16 +220,17 @@ void tile_kernel(const GroupedArgs g) {
     int at;
     if (i >= A::kLoads) {
       const int j = i - A::kLoads;
-      src = b_base + b_off[j];
+      src = b.base_of(b_base, j, b_ld) + b.off_of(j, (uint32_t)b_ld);
       at = BMODE == kRows ? B::piece_of(tid, j) * 8 : B::row_of(tid, j);
       la += A::kBytes + j * NT * 16;
     } else {
       if constexpr (MODE == kLinear && GATHER)
         src = a_ptr[i];
-      else if constexpr (MODE == kDw && GATHER)
-        src = (unsigned)tok[i] < (unsigned)g.T ? a_base + tok[i] * a_ld + a_off[i] : zeros;
-      else
-        src = a_base + a_off[i];
+      else if constexpr (MODE == kDw && GATHER) {
+        const int tk = token(i, tid);
+        src = (unsigned)tk < (unsigned)g.T ? a_base + tk * a_ld + a.off[i % A::kKinds] : zeros;
+      } else
+        src = a.base_of(a_base, i, a_ld) + a.off_of(i, (uint32_t)a_ld);
       at = AMODE == kRows ? A::piece_of(tid, i) * 8 : A::row_of(tid, i);
       la += i * NT * 16;
     }
@@ -242,7 +241,7 @@ void tile_kernel(const GroupedArgs g) {
     b_base += b_step;
     if constexpr (MODE == kDw && GATHER) {
       tok_row += kStage;
-      tok_left -= kStage;
+      tok_par ^= 1;
       load_tokens();
     }
   };
@@ -252,22 +251,15 @@ void tile_kernel(const GroupedArgs g) {
   // Loads of A that hold live rows when a tile's fragments are cut to nm of FM.
   auto a_loads = [&](int nm) MOE_INLINE { return AMODE == kRows ? div_up(A::kLoads * nm, FM) : A::kLoads; };
 
-  // The copies run two stages ahead of the arithmetic, through the items in the order taken:
-  // the item being copied (its number and index), what remains of its reduction (at least 1:
-  // an empty one is a stage of zeros), the live length of its partial stage and its fragment
-  // count.  The item after it is claimed when its own copies begin, so that the counter's
-  // answer is there when it is needed.
-  int cp_seq = 0, cp_idx = share(xcd) + (int)blockIdx.x / kXcds, cp_left = 0, cp_tail = 0,
-      cp_nm = FM;
-  int claimed = 0;  // thread 0: of this XCD's share
-  auto frags_of = [&](int rows) MOE_INLINE {  // fragments that are computed: FM, FM / 2 or FM / 4
-    return rows > BM / 2 ? FM : rows > BM / 4 ? FM / 2 : FM / 4;
+  // The copies run two stages ahead of the arithmetic, through this block's items in order: the
+  // item being copied, what remains of its reduction (at least 1: an empty one is a stage of
+  // zeros), the live length of its partial stage and its fragment count.
+  const int first = share(xcd) + (int)blockIdx.x / kXcds, last = share(xcd + 1);
+  int cp_idx = first, cp_left = 0, cp_tail = 0, cp_nm = FM;
+  auto frags_of = [&](int rows) MOE_INLINE {  // fragments that are computed: quarters of FM
+    return max(1, div_up(rows, BM / 4)) * (FM / 4);
   };
   auto begin_copies = [&]() MOE_INLINE {
-    if (g.claim && tid == 0)
-      claimed = __hip_atomic_fetch_add(g.claim + xcd, 1, __ATOMIC_RELAXED,
-                                       __HIP_MEMORY_SCOPE_AGENT);
-    meet();
     int tid_v = tid;  // through an empty statement, see the epilogue
     asm volatile("" : "+v"(tid_v));
     const Item t = find(cp_idx);
@@ -276,35 +268,16 @@ void tile_kernel(const GroupedArgs g) {
     cp_nm = frags_of(t.rows);
     cp_tail = t.red % kStage;
   };
-  auto copies_left = [&]() MOE_INLINE { return cp_idx >= 0; };  // block-uniform
+  auto copies_left = [&]() MOE_INLINE { return cp_idx < last; };  // block-uniform
   auto copies_done = [&]() MOE_INLINE {  // a stage was copied
     cp_left -= kStage;
     if (cp_left > 0) next_stage();
   };
   // On to the next item where the last one's stages are all copied.
   auto copies_next = [&]() MOE_INLINE {
-    if (cp_left > 0 || cp_idx < 0) return;
-    ++cp_seq;
-    if (tid == 0) {
-      int next = -1;
-      if (!g.claim) {
-        if (cp_idx + slots < share(xcd + 1)) next = cp_idx + slots;
-      } else {
-        // its own share, then what is left of the others'
-        for (int q = 0; q < kXcds && next < 0; ++q) {
-          const int o = (xcd + q) % kXcds;
-          if (q > 0)
-            claimed = __hip_atomic_fetch_add(g.claim + o, 1, __ATOMIC_RELAXED,
-                                             __HIP_MEMORY_SCOPE_AGENT);
-          if (claimed < share(o + 1) - share(o) - slots) next = share(o) + slots + claimed;
-        }
-      }
-      s_item[cp_seq & 3] = next;
-      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    }
-    block_barrier();
-    cp_idx = __builtin_amdgcn_readfirstlane(s_item[cp_seq & 3]);
-    if (cp_idx >= 0) begin_copies();
+    if (cp_left > 0 || cp_idx >= last) return;
+    cp_idx += slots;
+    if (cp_idx < last) begin_copies();
   };
   // A stage of any kind into a slot.
   auto copy_any = [&](int slot) MOE_INLINE {
@@ -363,9 +336,8 @@ void tile_kernel(const GroupedArgs g) {
     const uint32_t so = slot * kSlot;
 #pragma unroll
     for (int m = 0; m < NM; ++m) {
-      constexpr int per = (kReads + NM - 1) / NM;
 #pragma unroll
-      for (int q = m * per; q < (m + 1) * per && q < kReads; ++q) {
+      for (int q = m * kReads / NM; q < (m + 1) * kReads / NM; ++q) {
         if (q < FN) b1[q] = read_b(so, 1, q);
         else a1[q - FN] = read_a(so, 1, q - FN);
       }
@@ -520,18 +492,19 @@ void tile_kernel(const GroupedArgs g) {
           swap16(o.y, o.w);
           if (live) *(uint4*)(g.out + row + c) = o;
         }
+        if constexpr (MODE == kDx) __builtin_amdgcn_sched_barrier(0);
       }
     }
   };
 
-  if (cp_idx >= share(xcd + 1)) return;  // block-uniform
-  if (tid == 0) s_item[0] = cp_idx;
-  meet();
+  if (first >= last) return;  // block-uniform
   begin_copies();
+  if constexpr (MODE == kDw && GATHER) wait_copies();  // the first tokens
   copy_any(0);
   copies_done();
   copies_next();
   if (copies_left()) {
+    if constexpr (MODE == kDw && GATHER) wait_copies();
     copy_any(1);
     copies_done();
   }
@@ -540,9 +513,7 @@ void tile_kernel(const GroupedArgs g) {
   int slot = 0;
   using Yes = std::true_type;
   using No = std::false_type;
-  for (int seq = 0;; ++seq) {
-    const int idx = __builtin_amdgcn_readfirstlane(s_item[seq & 3]);
-    if (idx < 0) return;  // block-uniform
+  for (int idx = first; idx < last; idx += slots) {
     const Item cur = find(idx);
     const int nst = max(1, div_up(cur.red, kStage));
     auto run = [&](auto nm_c) MOE_INLINE {
@@ -557,8 +528,17 @@ void tile_kernel(const GroupedArgs g) {
       for (int m = 0; m < NM; ++m) a0[m] = read_a(slot * kSlot, 0, m);
       // Stages whose mid-point copies a whole stage of this same item: a loop without branches,
       // which the register allocator needs (with one it kept two sets of accumulators).
-      const int fast = cp_seq == seq ? max(cp_left, 0) / kStage : 0;
+      const int fast = cp_idx == idx ? max(cp_left, 0) / kStage : 0;
       int s = 0;
+      // The loop's addresses pass through an empty statement: one that was spilled is reloaded,
+      // and waited for, here and not in the loop, where the wait would be for the copies too.
+#pragma unroll
+      for (uint32_t& v : fa) asm volatile("" : "+v"(v));
+#pragma unroll
+      for (uint32_t& v : fb) asm volatile("" : "+v"(v));
+      if constexpr (!(MODE == kLinear && GATHER))
+        asm volatile("" : "+v"(a.off[0]), "+v"(a.off[1]));
+      asm volatile("" : "+v"(b.off[0]), "+v"(b.off[1]));
       for (; s < fast; ++s) {
         half0(slot, nm_c);
         wait_copies();
@@ -587,6 +567,8 @@ void tile_kernel(const GroupedArgs g) {
     const int nm = frags_of(cur.rows);
     if (nm == FM)
       run(std::integral_constant<int, FM>{});
+    else if (nm == 3 * FM / 4)
+      run(std::integral_constant<int, 3 * FM / 4>{});
     else if (nm == FM / 2)
       run(std::integral_constant<int, FM / 2>{});
     else
@@ -684,8 +666,6 @@ __global__ __launch_bounds__(256) void join_dw_kernel(const GroupedArgs g, int64
   *o = v;
 }
 
-__global__ void zero_claims_kernel(int* claim) { claim[threadIdx.x] = 0; }
-
 int cu_count() {
   static const int n = [] {
     int dev = 0, v = 0;
@@ -714,10 +694,6 @@ hipError_t run_grouped(const moe_grouped& p, GroupedArgs g, int mode, void* ws, 
   const GroupedPlan plan = grouped_plan(p, mode);
   g.split = plan.split;
   g.part = plan.split > 1 ? static_cast<float*>(ws) : nullptr;
-  if (plan.claims) {
-    g.claim = reinterpret_cast<int*>(static_cast<char*>(ws) + plan.part_bytes);
-    hipLaunchKernelGGL(zero_claims_kernel, dim3(1), dim3(kXcds), 0, s, g.claim);
-  }
   if (plan.kernel == kStream) {
     const hipError_t err = launch_grouped_stream(g, mode, s);
     if (err != hipSuccess) return err;
@@ -747,7 +723,7 @@ hipError_t run_grouped(const moe_grouped& p, GroupedArgs g, int mode, void* ws, 
 }  // namespace
 
 GroupedPlan grouped_plan(const moe_grouped& p, int mode) {
-  GroupedPlan plan{kTile64, 1, false, 0, 0};
+  GroupedPlan plan{kTile64, 1, 0};
   const int ncols = mode == kDx ? p.K : p.N, red = mode == kLinear ? p.K : mode == kDx ? p.N : p.R;
   const int64_t active = std::min(p.E, std::max(p.R, 1)), rows = p.R / p.E;
   auto tiles = [&](int bm, int bn) -> int64_t {
@@ -772,12 +748,10 @@ GroupedPlan grouped_plan(const moe_grouped& p, int mode) {
             : plan.kernel == kTile128 ? tiles(128, 128) : tiles(64, 128);
     const int64_t per_expert = mode == kDw ? red / p.E : red;
     plan.split = (int)std::max<int64_t>(1, std::min<int64_t>(per_expert / 256, slots / 2 / std::max<int64_t>(items, 1)));
-    plan.claims = plan.split == 1 && items > 4 * slots;
   }
   if (plan.split > 1)
-    plan.part_bytes = align256((size_t)plan.split * 4 *
-                               (mode == kDw ? (size_t)p.E * p.K * p.N : (size_t)p.R * ncols));
-  plan.ws_bytes = plan.part_bytes + (plan.claims ? kClaimBytes : 0);
+    plan.ws_bytes = align256((size_t)plan.split * 4 *
+                             (mode == kDw ? (size_t)p.E * p.K * p.N : (size_t)p.R * ncols));
   return plan;
 }
 
@@ -787,7 +761,7 @@ hipError_t launch_grouped_linear(const moe_grouped& p, const void* x, const int3
                                  void* ws, hipStream_t s) {
   GroupedArgs g{(const uint16_t*)x, (const uint16_t*)w, row_token, offsets, (const uint16_t*)bias,
                 (const uint16_t*)residual, (uint16_t*)y, nullptr, codes, scales, nullptr, nullptr,
-                p.R, p.T, p.K, p.N, p.E, act, 0, 1, nullptr, nullptr};
+                p.R, p.T, p.K, p.N, p.E, act, 0, 1, nullptr};
   return run_grouped(p, g, kLinear, ws, s);
 }
 
@@ -797,7 +771,7 @@ hipError_t launch_grouped_dx(const moe_grouped& p, const void* dz, const int32_t
   GroupedArgs g{(const uint16_t*)dz, (const uint16_t*)w, nullptr, offsets, nullptr, nullptr,
                 (uint16_t*)dx, (uint16_t*)a, const_cast<uint8_t*>(codes),
                 const_cast<uint8_t*>(scales), nullptr, nullptr, p.R, p.T, p.K, p.N, p.E, act, 0, 1,
-                nullptr, nullptr};
+                nullptr};
   return run_grouped(p, g, kDx, ws, s);
 }
 
@@ -806,7 +780,7 @@ hipError_t launch_grouped_dw(const moe_grouped& p, const void* x, const int32_t*
                              float* dbias, void* ws, hipStream_t s) {
   GroupedArgs g{(const uint16_t*)x, (const uint16_t*)dz, row_token, offsets, nullptr, nullptr,
                 nullptr, nullptr, nullptr, nullptr, dw, dbias, p.R, p.T, p.K, p.N, p.E, 0,
-                accumulate, 1, nullptr, nullptr};
+                accumulate, 1, nullptr};
   if (dbias)
     hipLaunchKernelGGL(dbias_kernel, dim3(div_up(p.N, 64), p.E), dim3(256), 0, s, g);
   return run_grouped(p, g, kDw, ws, s);
