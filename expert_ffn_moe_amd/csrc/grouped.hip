@@ -53,6 +53,7 @@ void tile_kernel(const GroupedArgs g) {
   __shared__ __align__(1024) char smem[2 * kSlot];
   __shared__ int s_start[kMaxE + 1];  // linear, dx: M tiles before each expert
   __shared__ int s_wsum[WM * WN];
+  __shared__ __align__(128) char s_stage[WM * WN * 2048];  // the epilogue's, see there
   __shared__ int s_tok[MODE == kDw && GATHER ? WM * WN * 128 : 1];
 
   const int tid = threadIdx.x, lane = tid & 63;
@@ -110,10 +111,11 @@ void tile_kernel(const GroupedArgs g) {
       local = item - per_tile * start(lo);
     }
     segment(g.offsets, g.R, t.e, beg, end);
-    constexpr int kGroup = 8;
-    const int group = local / (kGroup * per_tile) * kGroup;
+    // a weight gradient over few rows is its output: tile after tile of the same rows of dW
+    const int grouped = MODE == kDw && end - beg < 4096 ? 1 : 8;
+    const int group = local / (grouped * per_tile) * grouped;
     local -= group * per_tile;
-    const int in_group = min(kGroup, tiles - group), nt = local / in_group;
+    const int in_group = min(grouped, tiles - group), nt = local / in_group;
     const int mt = group + local - nt * in_group;
     if constexpr (MODE == kDw) {
       t.m0 = mt * BM;
@@ -380,23 +382,43 @@ void tile_kernel(const GroupedArgs g) {
     asm volatile("" : "+v"(lane));
     const int c4 = t.n0 + wcol + 4 * (lane >> 4);
     if (MODE == kDw || g.split > 1) {
-      // fp32: the weight gradients, or a part's sums for the joining kernel
+      // fp32: the weight gradients, or a part's sums for the joining kernel.  Straight from the
+      // registers a store instruction would write 64 bytes of each of 16 rows; through 2 KiB of
+      // LDS of the wavefront's own (laid out like a kRows operand: 16 rows x 128 bytes) it
+      // writes whole 128-byte lines (dW of 128 experts 2048 x 768, 805 MB: 274 -> 246 us, with
+      // the non-temporal hint 192 us).
       const size_t row0 = MODE == kDw ? ((size_t)t.part * g.E + t.e) * g.K + t.m0
                                       : (size_t)t.part * g.R + t.m0;
-      float* const base = (g.split > 1 ? g.part : g.dw) + row0 * ncols + c4;
+      const int lr = lane >> 3, c = t.n0 + wcol + (lane & 7) * 4;
+      float* const base = (g.split > 1 ? g.part : g.dw) + row0 * ncols + c;
       const bool add = MODE == kDw && g.split == 1 && g.accumulate;
+      const uint32_t st = (uint32_t)(uintptr_t)(MOE_LDS char*)s_stage + wave * 2048;
+      const int fr = lane & 15, fs = rows_swizzle(fr);
 #pragma unroll
       for (int m = 0; m < FM; ++m) {
         if (m >= nm) break;
-        const int r = (m * WM + wm) * 16 + (lane & 15);
-        if (r >= t.rows) continue;
-        float* o = base + (size_t)r * ncols;
 #pragma unroll
-        for (int n = 0; n < FN; ++n) {
-          if (c4 + 16 * n >= ncols) continue;
-          f32x4_t v = acc[m][n];
-          if (add) v += *(const f32x4_t*)(o + 16 * n);
-          *(f32x4_t*)(o + 16 * n) = v;
+        for (int n = 0; n < FN; n += 2) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            *(MOE_LDS f32x4_t*)(uintptr_t)(st + fr * 128 + (((h * 4 + (lane >> 4)) ^ fs) * 16)) =
+                acc[m][n + h];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int lrow = h * 8 + lr, r = (m * WM + wm) * 16 + lrow;
+            f32x4_t v = *(MOE_LDS const f32x4_t*)(uintptr_t)(
+                st + lrow * 128 + (((lane & 7) ^ rows_swizzle(lrow)) * 16));
+            if (r < t.rows && c + 16 * n < ncols) {
+              float* const o = base + (size_t)r * ncols + 16 * n;
+              if (add) v += *(const f32x4_t*)o;
+              // the gradients are written once and are far larger than the caches; a part's
+              // sums are read again at once
+              if (MODE == kDw && g.split == 1)
+                __builtin_nontemporal_store(v, (f32x4_t*)o);
+              else
+                *(f32x4_t*)o = v;
+            }
+          }
         }
       }
       return;
@@ -724,30 +746,47 @@ hipError_t run_grouped(const moe_grouped& p, GroupedArgs g, int mode, void* ws, 
 
 GroupedPlan grouped_plan(const moe_grouped& p, int mode) {
   GroupedPlan plan{kTile64, 1, 0};
-  const int ncols = mode == kDx ? p.K : p.N, red = mode == kLinear ? p.K : mode == kDx ? p.N : p.R;
-  const int64_t active = std::min(p.E, std::max(p.R, 1)), rows = p.R / p.E;
+  const int ncols = mode == kDx ? p.K : p.N, red = mode == kLinear ? p.K : p.N;
+  const int64_t rows = p.R / p.E, active = std::min(p.E, std::max(p.R, 1));
+  // tiles, with half of the experts having one more than their rows need
   auto tiles = [&](int bm, int bn) -> int64_t {
     const int64_t mt = mode == kDw ? (int64_t)p.E * div_up(p.K, bm)
                                    : std::max<int64_t>(active, p.R / bm + (p.E > 1 ? p.E / 2 : 1));
     return mt * div_up(ncols, bn);
   };
-  const int64_t sblocks = active * div_up(ncols, kStreamCols);
-  int64_t items;
-  if (mode != kDw && p.R <= 16 * (int64_t)p.E && sblocks <= 1536) {
-    plan.kernel = kStream;
-    // parts of at least 512 of the reduction, up to a block per CU
-    plan.split = (int)std::max<int64_t>(1, std::min<int64_t>(red / 512, 256 / sblocks));
-    items = 0;
-  } else {
-    if ((mode == kDw || rows > 448) && tiles(256, 256) >= 256)
+  const int64_t n256 = tiles(256, 256), n128 = tiles(128, 128), n64 = tiles(64, 128);
+  const int64_t stream = active * div_up(ncols, kStreamCols);
+  auto parts = [](int64_t a, int64_t b) { return (int)std::max<int64_t>(1, std::min(a, b)); };
+  if (mode == kDw) {
+    // 256-tiles where they fill the chip (2048 x 768 x 128 experts: 192 us against 221 us with
+    // 128-tiles); else over many rows 128-tiles and the rows split (one 2048 x 768 over 16384
+    // rows: 131 -> 65 us with 5 parts); over few rows the smallest that fill it
+    if (n256 >= 192) {
       plan.kernel = kTile256;
-    else if (tiles(128, 128) >= 256)
+    } else if (rows >= 1024) {
       plan.kernel = kTile128;
-    const int slots = plan.kernel == kTile256 ? 256 : plan.kernel == kTile128 ? 512 : 768;
-    items = plan.kernel == kTile256 ? tiles(256, 256)
-            : plan.kernel == kTile128 ? tiles(128, 128) : tiles(64, 128);
-    const int64_t per_expert = mode == kDw ? red / p.E : red;
-    plan.split = (int)std::max<int64_t>(1, std::min<int64_t>(per_expert / 256, slots / 2 / std::max<int64_t>(items, 1)));
+      plan.split = parts(rows / 512, 512 / n128);
+    } else if (n128 >= 256) {
+      plan.kernel = kTile128;
+    }
+  } else if (p.R <= 16 * (int64_t)p.E && stream <= (mode == kDx ? 512 : 1536)) {
+    // few rows, few weights: latency.  (4 rows for each of 64 experts of 4096 x 1408: 129 us, with
+    // 128-tiles 146 us; 256 experts of 7168 x 2048: 1.40 and 1.25 ms.  dx, 2 rows for each of 32
+    // experts of 2048 x 2048: 61 and 42 us; 16 rows of one 4096 x 4096: 13 and 32 us.)
+    plan.kernel = kStream;
+    plan.split = parts(red / 1024, 256 / stream);
+    if (plan.split < 3 && mode == kLinear) plan.split = 1;  // the joining launch costs as much
+  } else if (rows > 448 && n256 >= 256) {
+    // (406 rows per expert, 4096 -> 1408: 458 us with 128-tiles, 498 us with 256-tiles; 512
+    // rows, 7168 -> 2048: 5.2 ms and 4.0 ms)
+    plan.kernel = kTile256;
+  } else if (n128 >= 384) {
+    // (4000 x 2048 x 2048: 41 us, 52 us with 64-tiles; 1003 x 1416 x 2056, 136 tiles: 26 us and
+    // 22 us)
+    plan.kernel = kTile128;
+  } else {
+    // few tiles: long reductions in parts (100 x 7168 x 1024: 36 -> 16 us)
+    plan.split = parts(red / 1024, 256 / n64);
   }
   if (plan.split > 1)
     plan.ws_bytes = align256((size_t)plan.split * 4 *
