@@ -574,12 +574,19 @@ def routing_buffers(p: Problem, device="cuda"):
 @dataclasses.dataclass(frozen=True)
 class GroupedProblem:
     """Shapes of a grouped linear product: R rows in the layout, K -> N, E experts; T: rows of
-    x when it is read through row_token (default R)."""
+    x when it is read through row_token (default R).  Keep it between calls: it also holds what
+    they derive from the shapes."""
     R: int
     K: int
     N: int
     E: int = 1
     T: Optional[int] = None
+
+    def __post_init__(self):
+        c = MoeGrouped(self.R, self.x_tokens, self.K, self.N, self.E)
+        object.__setattr__(self, "_c", c)
+        object.__setattr__(self, "_ref", ctypes.byref(c))
+        object.__setattr__(self, "_ws_bytes", {})
 
     def c(self) -> MoeGrouped:
         return MoeGrouped(self.R, self.x_tokens, self.K, self.N, self.E)
@@ -589,12 +596,13 @@ class GroupedProblem:
         return self.R if self.T is None else self.T
 
     def check(self) -> int:
-        c = self.c()
-        return lib.moe_grouped_check(ctypes.byref(c))
+        return lib.moe_grouped_check(self._ref)
 
     def workspace_bytes(self, op: int) -> int:
-        c = self.c()
-        return int(lib.moe_grouped_workspace_bytes(ctypes.byref(c), op))
+        n = self._ws_bytes.get(op)
+        if n is None:
+            n = self._ws_bytes[op] = int(lib.moe_grouped_workspace_bytes(self._ref, op))
+        return n
 
 
 def grouped_workspace(p: GroupedProblem, op: int, device="cuda"):
@@ -612,35 +620,69 @@ def checkpoint_buffers(rows: int, cols: int, device="cuda"):
 
 
 def _act(name: str) -> int:
-    if name not in ACTIVATIONS:
+    act = ACTIVATIONS.get(name)
+    if act is None:
         raise ValueError(f"unknown activation {name!r}; one of {', '.join(ACTIVATIONS)}")
-    return ACTIVATIONS[name]
+    return act
 
 
-def _need_all(first: torch.Tensor, **named):
-    """named: (tensor or None, shape, dtype); all on the device of `first`."""
-    for name, (t, shape, dtype) in named.items():
-        if t is not None:
-            _need(t, name, shape, dtype)
-            if t.device != first.device:
-                raise ValueError(f"{name} is on {t.device}, expected {first.device}")
+def _arg(t, name: str, shape, dtype, index: int):
+    """The address of an argument on GPU `index` after its checks (None for None).  The call of
+    a small product takes about as long as this marshalling, hence one pass of cheap tests, and
+    the words only where one fails."""
+    if t is None:
+        return None
+    try:
+        if (t.dtype is dtype and t.get_device() == index and t.shape == shape
+                and t.is_contiguous()):
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _need(t, name, shape, dtype)
+    raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
 
 
-def _grouped_call(name: str, p: GroupedProblem, op: int, ws, device, *args):
-    """The call on the current stream of the tensors' device, with a workspace if it needs one."""
+def _first(t, name: str, shape, dtype) -> int:
+    """The GPU of a call: that of its first tensor, which _arg then checks like the others."""
+    index = t.get_device() if isinstance(t, torch.Tensor) else -1
+    if index < 0:
+        _need(t, name, shape, dtype)
+    return index
+
+
+# the current stream's handle; the public torch.cuda.current_stream() builds an object around it
+# in 3.5 us, as long as a small call's launch takes
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _launch(name: str, index: int, *args):
+    """The call on the current stream of GPU `index`."""
+    if index == torch.cuda.current_device():
+        st = getattr(lib, name)(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(index):
+            st = getattr(lib, name)(*args, _raw_stream(index))
+    if st != MOE_OK:
+        raise MoeError(name, st)
+
+
+def _grouped_ws(p: GroupedProblem, op: int, ws, t):
+    """(workspace or None, its address, its bytes) of a call on the GPU of tensor t"""
     if ws is None:
-        ws = grouped_workspace(p, op, device)
-    elif ws.device != device or ws.dtype != torch.uint8 or not ws.is_contiguous():
-        raise ValueError(f"ws must be a contiguous uint8 tensor on {device}")
-    c = p.c()
-    with torch.cuda.device(device):
-        _call(name, ctypes.byref(c), *args, _ptr(ws), 0 if ws is None else ws.numel(), _stream())
+        n = p.workspace_bytes(op)
+        if n == 0:
+            return None, None, 0
+        ws = torch.empty(n, dtype=torch.uint8, device=t.device)
+    elif ws.dtype != torch.uint8 or ws.device != t.device or not ws.is_contiguous():
+        raise ValueError(f"ws must be a contiguous uint8 tensor on {t.device}")
+    return ws, ws.data_ptr(), ws.numel()
 
 
-def _grouped_common(p: GroupedProblem, offsets):
+def _offsets_arg(p: GroupedProblem, offsets, index: int):
     if offsets is None and p.E != 1:
         raise ValueError("offsets may be left out only with one expert")
-    return (offsets, (p.E + 1,), torch.int32)
+    return _arg(offsets, "offsets", (p.E + 1,), torch.int32, index)
 
 
 def grouped_linear(p: GroupedProblem, x, w, offsets=None, bias=None, act: str = "none",
@@ -649,18 +691,18 @@ def grouped_linear(p: GroupedProblem, x, w, offsets=None, bias=None, act: str = 
     [T, K] read through row_token).  checkpoint: None, or the (codes, scales) buffers that
     receive the pre-activations in 8 bits.  Returns y [R, N]; rows behind the last expert's
     are left as they were."""
-    bf = torch.bfloat16
+    bf, R, K, N = torch.bfloat16, p.R, p.K, p.N
+    xs = (R if row_token is None else p.x_tokens, K)
+    dev = _first(x, "x", xs, bf)
+    y = _empty((R, N), bf, x.device) if out is None else out
     codes, scales = checkpoint if checkpoint is not None else (None, None)
-    _need(x, "x", (p.R if row_token is None else p.x_tokens, p.K), bf)
-    y = _empty((p.R, p.N), bf, x.device) if out is None else out
-    _need_all(x, w=(w, (p.E, p.K, p.N), bf), offsets=_grouped_common(p, offsets),
-              bias=(bias, (p.E, p.N), bf), residual=(residual, (p.R, p.N), bf),
-              row_token=(row_token, (p.R,), torch.int32), out=(y, (p.R, p.N), bf),
-              codes=(codes, (p.R, p.N), torch.uint8),
-              scales=(scales, (p.R, p.N // QBLOCK), torch.uint8))
-    _grouped_call("moe_grouped_linear", p, OP_GROUPED_LINEAR, ws, x.device, _ptr(x),
-                  _ptr(row_token), _ptr(offsets), _ptr(w), _ptr(bias), _act(act),
-                  _ptr(residual), _ptr(y), _ptr(codes), _ptr(scales))
+    ws, wsp, wsn = _grouped_ws(p, OP_GROUPED_LINEAR, ws, x)
+    _launch("moe_grouped_linear", dev, p._ref, _arg(x, "x", xs, bf, dev),
+            _arg(row_token, "row_token", (R,), torch.int32, dev), _offsets_arg(p, offsets, dev),
+            _arg(w, "w", (p.E, K, N), bf, dev), _arg(bias, "bias", (p.E, N), bf, dev), _act(act),
+            _arg(residual, "residual", (R, N), bf, dev), _arg(y, "out", (R, N), bf, dev),
+            _arg(codes, "codes", (R, N), torch.uint8, dev),
+            _arg(scales, "scales", (R, N // QBLOCK), torch.uint8, dev), wsp, wsn)
     return y
 
 
@@ -669,17 +711,17 @@ def grouped_linear_dx(p: GroupedProblem, dz, w, offsets=None, act: str = "none",
     """dx[r] = (dz[r] w[e]^T) * act'(z[r]) with z [R, K] from the checkpoint of the product
     whose activation made x (None: dz w^T alone); a, if given, receives act(z) [R, K].
     Returns dx [R, K]."""
-    bf = torch.bfloat16
+    bf, R, K, N = torch.bfloat16, p.R, p.K, p.N
+    dev = _first(dz, "dz", (R, N), bf)
+    dx = _empty((R, K), bf, dz.device) if out is None else out
     codes, scales = checkpoint if checkpoint is not None else (None, None)
-    _need(dz, "dz", (p.R, p.N), bf)
-    dx = _empty((p.R, p.K), bf, dz.device) if out is None else out
-    _need_all(dz, w=(w, (p.E, p.K, p.N), bf), offsets=_grouped_common(p, offsets),
-              codes=(codes, (p.R, p.K), torch.uint8),
-              scales=(scales, (p.R, p.K // QBLOCK), torch.uint8), out=(dx, (p.R, p.K), bf),
-              a=(a, (p.R, p.K), bf))
-    _grouped_call("moe_grouped_linear_dx", p, OP_GROUPED_DX, ws, dz.device, _ptr(dz),
-                  _ptr(offsets), _ptr(w), _act(act), _ptr(codes), _ptr(scales), _ptr(dx),
-                  _ptr(a))
+    ws, wsp, wsn = _grouped_ws(p, OP_GROUPED_DX, ws, dz)
+    _launch("moe_grouped_linear_dx", dev, p._ref, _arg(dz, "dz", (R, N), bf, dev),
+            _offsets_arg(p, offsets, dev),
+            _arg(w, "w", (p.E, K, N), bf, dev), _act(act),
+            _arg(codes, "codes", (R, K), torch.uint8, dev),
+            _arg(scales, "scales", (R, K // QBLOCK), torch.uint8, dev),
+            _arg(dx, "out", (R, K), bf, dev), _arg(a, "a", (R, K), bf, dev), wsp, wsn)
     return dx
 
 
@@ -689,19 +731,21 @@ def grouped_linear_dw(p: GroupedProblem, x, dz, offsets=None, row_token=None,
     """dw[e] = x_e^T dz_e [E, K, N] and dbias[e] = the column sums of dz_e [E, N], in fp32
     (accumulate: added to what dw and dbias hold, which must be given).  Returns (dw, dbias);
     dbias None unless asked for or passed in."""
-    bf, f32 = torch.bfloat16, torch.float32
-    _need(x, "x", (p.R if row_token is None else p.x_tokens, p.K), bf)
+    bf, f32, R, K, N = torch.bfloat16, torch.float32, p.R, p.K, p.N
     if accumulate and (dw is None or (want_bias and dbias is None)):
         raise ValueError("accumulate needs the gradients to add to")
-    dw = _empty((p.E, p.K, p.N), f32, x.device) if dw is None else dw
+    xs = (R if row_token is None else p.x_tokens, K)
+    dev = _first(x, "x", xs, bf)
+    if dw is None:
+        dw = _empty((p.E, K, N), f32, x.device)
     if dbias is None and want_bias:
-        dbias = _empty((p.E, p.N), f32, x.device)
-    _need_all(x, dz=(dz, (p.R, p.N), bf), offsets=_grouped_common(p, offsets),
-              row_token=(row_token, (p.R,), torch.int32), dw=(dw, (p.E, p.K, p.N), f32),
-              dbias=(dbias, (p.E, p.N), f32))
-    _grouped_call("moe_grouped_linear_dw", p, OP_GROUPED_DW, ws, x.device, _ptr(x),
-                  _ptr(row_token), _ptr(dz), _ptr(offsets), int(bool(accumulate)), _ptr(dw),
-                  _ptr(dbias))
+        dbias = _empty((p.E, N), f32, x.device)
+    ws, wsp, wsn = _grouped_ws(p, OP_GROUPED_DW, ws, x)
+    _launch("moe_grouped_linear_dw", dev, p._ref, _arg(x, "x", xs, bf, dev),
+            _arg(row_token, "row_token", (R,), torch.int32, dev),
+            _arg(dz, "dz", (R, N), bf, dev), _offsets_arg(p, offsets, dev),
+            1 if accumulate else 0, _arg(dw, "dw", (p.E, K, N), f32, dev),
+            _arg(dbias, "dbias", (p.E, N), f32, dev), wsp, wsn)
     return dw, dbias
 
 
@@ -711,16 +755,15 @@ def activation_backward(dy, checkpoint, act: str, live_rows=None, out=None, a=No
     were.  Returns dz, shaped as dy [rows, cols]."""
     if dy.dim() != 2:
         raise ValueError("dy must be 2-D")
-    bf = torch.bfloat16
-    rows, cols = dy.shape
+    bf, shape = torch.bfloat16, dy.shape
+    rows, cols = shape
+    dev = _first(dy, "dy", shape, bf)
     codes, scales = checkpoint
-    _need(dy, "dy", (rows, cols), bf)
-    dz = _empty((rows, cols), bf, dy.device) if out is None else out
-    _need_all(dy, codes=(codes, (rows, cols), torch.uint8),
-              scales=(scales, (rows, cols // QBLOCK), torch.uint8), out=(dz, (rows, cols), bf),
-              a=(a, (rows, cols), bf), live_rows=(live_rows, (1,), torch.int32))
-    with torch.cuda.device(dy.device):
-        _call("moe_activation_backward", ctypes.c_int64(rows), ctypes.c_int32(cols),
-              _ptr(live_rows), _act(act), _ptr(dy), _ptr(codes), _ptr(scales), _ptr(dz), _ptr(a),
-              _stream())
+    dz = _empty(shape, bf, dy.device) if out is None else out
+    _launch("moe_activation_backward", dev, rows, cols,
+            _arg(live_rows, "live_rows", (1,), torch.int32, dev), _act(act),
+            _arg(dy, "dy", shape, bf, dev),
+            _arg(codes, "codes", shape, torch.uint8, dev),
+            _arg(scales, "scales", (rows, cols // QBLOCK), torch.uint8, dev),
+            _arg(dz, "out", shape, bf, dev), _arg(a, "a", shape, bf, dev))
     return dz
