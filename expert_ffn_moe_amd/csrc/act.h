@@ -10,7 +10,11 @@
 
 namespace moe {
 
-__device__ __forceinline__ float sigmoid(float z) { return 1.0f / (1.0f + __expf(-z)); }
+// The hardware reciprocal (1 ulp) in place of the exact division's ten instructions; results
+// below the normal range are zero.
+__device__ __forceinline__ float sigmoid(float z) {
+  return __builtin_amdgcn_rcpf(1.0f + __expf(-z));
+}
 
 // gelu in its tanh form, 0.5 z (1 + tanh u) = z sigma(2 u) with u = r (z + c z^3).
 constexpr float kGeluR2 = 1.5957691216057308f;  // 2 sqrt(2 / pi)
@@ -70,10 +74,12 @@ __device__ __forceinline__ void unpack_ckpt4(uint32_t w, int scale, float z[4]) 
   typedef float f32x2_t __attribute__((ext_vector_type(2)));
   const f32x2_t lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, false);
   const f32x2_t hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, true);
-  z[0] = ldexpf(lo[0], scale - 127);
-  z[1] = ldexpf(lo[1], scale - 127);
-  z[2] = ldexpf(hi[0], scale - 127);
-  z[3] = ldexpf(hi[1], scale - 127);
+  // 2^(scale - 127) as a float: byte 0 lies below the normal range
+  const float f = __uint_as_float(scale > 0 ? (uint32_t)scale << 23 : 0x00400000u);
+  z[0] = lo[0] * f;
+  z[1] = lo[1] * f;
+  z[2] = hi[0] * f;
+  z[3] = hi[1] * f;
 }
 
 }  // namespace moe

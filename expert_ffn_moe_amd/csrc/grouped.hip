@@ -625,28 +625,29 @@ __global__ __launch_bounds__(256) void dbias_kernel(const GroupedArgs g) {
   *d = g.accumulate ? *d + v : v;
 }
 
-// One 32-column block per thread.
+// 8 columns per thread: bound by memory, 7 bytes per value with a.
 __global__ __launch_bounds__(256) void act_backward_kernel(
-    int64_t nblocks, int kb, const int32_t* __restrict__ live, int act,
-    const uint16_t* __restrict__ dy, const uint8_t* __restrict__ codes,
-    const uint8_t* __restrict__ scales, uint16_t* __restrict__ dz, uint16_t* __restrict__ a) {
-  if (live) nblocks = min(nblocks, (int64_t)max(*live, 0) * kb);
-  for (int64_t b = (int64_t)blockIdx.x * 256 + threadIdx.x; b < nblocks;
-       b += (int64_t)gridDim.x * 256) {
-    for (int c = 0; c < 32; c += 8) {
-      float z[8], d[8], f[8];
-      unpack_ckpt4(*(const uint32_t*)(codes + b * 32 + c), scales[b], z);
-      unpack_ckpt4(*(const uint32_t*)(codes + b * 32 + c + 4), scales[b], z + 4);
-      unpack8(*(const uint4*)(dy + b * 32 + c), d);
-      for (int i = 0; i < 8; ++i) {
-        float df;
-        act_both(act, z[i], f[i], df);
-        d[i] *= df;
-      }
-      *(uint4*)(dz + b * 32 + c) = pack8(d);
-      if (a) *(uint4*)(a + b * 32 + c) = pack8(f);
-    }
+    int64_t n8, int cols8, const int32_t* __restrict__ live, int act,
+    const uint4* __restrict__ dy, const uint2* __restrict__ codes,
+    const uint8_t* __restrict__ scales, uint4* __restrict__ dz, uint4* __restrict__ a) {
+  if (live) n8 = min(n8, (int64_t)max(*live, 0) * cols8);
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= n8) return;
+  const uint2 q = codes[i];
+  const int s = scales[i >> 2];
+  const uint4 y = dy[i];
+  float z[8], d[8], f[8];
+  unpack_ckpt4(q.x, s, z);
+  unpack_ckpt4(q.y, s, z + 4);
+  unpack8(y, d);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    float df;
+    act_both(act, z[k], f[k], df);
+    d[k] *= df;
   }
+  dz[i] = pack8(d);
+  if (a) a[i] = pack8(f);
 }
 
 // Adds the parts of a split linear or dx in order and finishes: 4 columns per thread, a row's
@@ -830,10 +831,11 @@ size_t grouped_ws_bytes(const moe_grouped& p, int op) { return grouped_plan(p, o
 hipError_t launch_act_backward(int64_t rows, int cols, const int32_t* live, int act,
                                const void* dy, const uint8_t* codes, const uint8_t* scales,
                                void* dz, void* a, hipStream_t s) {
-  const int64_t nblocks = rows * (cols / kQBlock);
-  const int grid = (int)std::min<int64_t>(div_up64(nblocks, 256), 8192);
-  hipLaunchKernelGGL(act_backward_kernel, dim3(grid), dim3(256), 0, s, nblocks, cols / kQBlock,
-                     live, act, (const uint16_t*)dy, codes, scales, (uint16_t*)dz, (uint16_t*)a);
+  const int64_t n8 = rows * (cols / 8);
+  if (div_up64(n8, 256) > INT32_MAX) return hipErrorInvalidValue;  // (refused by the caller)
+  hipLaunchKernelGGL(act_backward_kernel, dim3((unsigned)div_up64(n8, 256)), dim3(256), 0, s, n8,
+                     cols / 8, live, act, (const uint4*)dy, (const uint2*)codes, scales,
+                     (uint4*)dz, (uint4*)a);
   return hipGetLastError();
 }
 

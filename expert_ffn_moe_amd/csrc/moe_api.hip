@@ -1027,7 +1027,8 @@ int moe_grouped_linear_dw(const moe_grouped* g, const void* x, const int32_t* ro
 int moe_activation_backward(int64_t rows, int32_t cols, const int32_t* live_rows, int act,
                             const void* dy, const uint8_t* z_codes, const uint8_t* z_scales,
                             void* dz, void* a, void* stream) {
-  if (rows < 0 || rows > ((int64_t)1 << 40) || cols < 1 || cols % kCkptBlock || !act_ok(act) ||
+  if (rows < 0 || rows > ((int64_t)1 << 39) / std::max(cols, 1) || cols < 1 ||
+      cols % kCkptBlock || !act_ok(act) ||
       (rows > 0 && (!dy || !z_codes || !z_scales || !dz)))
     return MOE_ERR_INVALID_ARG;
   if (!aligned16(dy) || !aligned16(z_codes) || !aligned16(dz) || !aligned16(a))

@@ -448,7 +448,8 @@ int moe_layer_backward(const moe_problem* p, const void* x, const float* logits,
  * belong to the one expert.  Rows >= offsets[E] are neither read nor written.
  *
  * Everything is bf16 (fp32 accumulation, each stored bf16 value rounded once) except the
- * weight and bias gradients, which are fp32.  Every result is deterministic.
+ * weight and bias gradients, which are fp32.  Every result is deterministic.  A sigmoid below
+ * 2^-126 counts as zero.
  * The kernels take offsets as clamped to [0, R], and read zeros for a row whose row_token
  * lies outside [0, T); the debug library reports both (moe_debug_status bits 2 and 3).
  *
@@ -541,7 +542,7 @@ int moe_grouped_linear_dw(const moe_grouped* g, const void* x, const int32_t* ro
  *   dy, dz [rows, cols] bf16; z_codes [rows, cols], z_scales [rows, cols/32]; a [rows, cols]
  *   bf16 or NULL; live_rows: device pointer (offsets + E), or NULL: all rows.
  * rows = 0 enqueues nothing.  MOE_ERR_INVALID_ARG: rows < 0, cols not a positive multiple of
- * 32, an unknown act.
+ * 32, rows * cols > 2^39, an unknown act.
  * --------------------------------------------------------------------------------- */
 int moe_activation_backward(int64_t rows, int32_t cols, const int32_t* live_rows, int act,
                             const void* dy, const uint8_t* z_codes, const uint8_t* z_scales,

@@ -35,13 +35,22 @@ def sigmoid_arg(z, act):
     return 0 * z
 
 
+def flushed(z, act):
+    """A sigmoid below the normal range, 2^-126, may be zero: that times the factors it has in
+    act and act', z (and gelu's argument's slope, 2 r (1 + 3 c z^2))."""
+    if act not in ("silu", "gelu_tanh"):
+        return 0 * z
+    return 2.0 ** -126 * (2 + z.abs() * (1.6 + 0.22 * z * z))
+
+
 def act_tol(z, f, dz_tol, act):
     """Bound of act's error at z known up to dz_tol: its slope (at most 1.13 for silu and gelu,
     2 |z| for relu2) times dz_tol, and its own evaluation: the argument of exp is off by
     3 * 2^-23 of itself, which is the relative error that exp makes of it, and the ten
     roundings around it."""
     slope = 2 * (z.abs() + dz_tol) if act == "relu2" else 1.13
-    return slope * dz_tol + (3 * sigmoid_arg(z, act) + 16) * 2.0 ** -23 * f.abs()
+    return (slope * dz_tol + (3 * sigmoid_arg(z, act) + 16) * 2.0 ** -23 * f.abs() +
+            flushed(z, act))
 
 
 def dact_tol(z, df, act):
@@ -52,7 +61,7 @@ def dact_tol(z, df, act):
     big = df.abs() + 1 + z.abs() * (1 if act == "silu" else 0)
     if act == "gelu_tanh":  # the second term: z s (1 - s) 2 r (1 + 3 c z^2), bounded by 1.1
         big = df.abs() + 2.2
-    return (3 * sigmoid_arg(z, act) + 32) * 2.0 ** -23 * big
+    return (3 * sigmoid_arg(z, act) + 32) * 2.0 ** -23 * big + flushed(z, act)
 
 
 def stored(ref, tol):

@@ -110,7 +110,7 @@ def test_activation_backward_refusals():
         return m.lib.moe_activation_backward(rows, cols, live, act, dy, zc, zs, dz, a, None)
 
     off8 = ctypes.c_void_p(dy.value + 8)
-    for kw in (dict(rows=-1), dict(cols=0), dict(cols=48), dict(act=5), dict(dy=None),
+    for kw in (dict(rows=-1), dict(rows=1 << 39), dict(cols=0), dict(cols=-32), dict(cols=48), dict(act=5), dict(dy=None),
                dict(zc=None), dict(zs=None), dict(dz=None), dict(dy=off8), dict(zc=off8),
                dict(dz=off8), dict(a=off8), dict(dz=dy), dict(a=dz), dict(a=zc), dict(dz=live)):
         assert go(**kw) == m.MOE_ERR_INVALID_ARG, kw
