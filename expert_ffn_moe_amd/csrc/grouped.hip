@@ -37,9 +37,9 @@ __device__ __forceinline__ void meet() { asm volatile(""); }
 
 // Persistent.  The items are ordered expert by expert, within an expert by groups of 8 M tiles,
 // within a group N tile by N tile (and part by part of a split reduction) with the M tiles
-// innermost, and cut into 8 shares, one per XCD (workgroups go to XCDs round-robin); a block
-// takes every n-th item of its XCD's share, so that the operand bytes that neighbouring items
-// share (8 x 4 tiles at a time of a dense product) come from that XCD's L2.
+// innermost, and cut into 8 shares of equal cost, one per XCD (workgroups go to XCDs
+// round-robin); a block takes every n-th item of its XCD's share, so that the operand bytes that
+// neighbouring items share (8 x 4 tiles at a time of a dense product) come from that XCD's L2.
 template <int MODE, bool GATHER, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2, 2)))
 void tile_kernel(const GroupedArgs g) {
@@ -51,8 +51,10 @@ void tile_kernel(const GroupedArgs g) {
   using B = Operand<BMODE, BN, NT>;
   constexpr int kSlot = A::kBytes + B::kBytes;
   __shared__ __align__(1024) char smem[2 * kSlot];
-  __shared__ int s_start[kMaxE + 1];  // linear, dx: M tiles before each expert
+  __shared__ int s_start[MODE == kDw ? 1 : kMaxE + 1];  // linear, dx: M tiles before each expert
   __shared__ int s_wsum[WM * WN];
+  __shared__ int64_t s_wcost[WM * WN];
+  __shared__ int s_share[kXcds + 1];  // first item of each XCD's share
   __shared__ __align__(128) char s_stage[WM * WN * 2048];  // the epilogue's, see there
   __shared__ int s_tok[MODE == kDw && GATHER ? WM * WN * 128 : 1];
 
@@ -63,34 +65,71 @@ void tile_kernel(const GroupedArgs g) {
   const int ncols = MODE == kDx ? g.K : g.N;
   const int ntn = div_up(ncols, BN), per_tile = ntn * g.split;  // items per M tile
 
-  // ---- all items, and this XCD's share of them
+  // ---- the M tiles before each expert, and this XCD's share of the items: an eighth of what
+  // they cost, in rows (linear, dx: a tile's own time is that of 3/4 of its height more than its
+  // rows') or stages (dw: storing a tile takes about 6) of an expert's items
   const int xcd = blockIdx.x % kXcds, slots = gridDim.x / kXcds;
-  int total;
-  if constexpr (MODE == kDw) {
-    total = g.E * div_up(g.K, BM) * per_tile;
-  } else {
+  {
+    const int ntk = div_up(g.K, BM);
+    auto cost_of = [&](int len, int tiles) MOE_INLINE {
+      return MODE == kDw ? (int64_t)(div_up(len, kStage) + 6) : (int64_t)len + tiles * (BM * 3 / 4);
+    };
     const int per = div_up(g.E, NT);
     const int e0 = min(g.E, tid * per), e1 = min(g.E, e0 + per);
     int sum = 0, lo, hi;
+    int64_t cost = 0;
     for (int e = e0; e < e1; ++e) {
       segment(g.offsets, g.R, e, lo, hi);
-      sum += div_up(hi - lo, BM);
+      const int tiles = MODE == kDw ? ntk : div_up(hi - lo, BM);
+      sum += tiles;
+      cost += cost_of(hi - lo, tiles);
     }
-    const int inc = wave_inclusive_scan(sum);
-    if (lane == 63) s_wsum[wave] = inc;
+    int inc = sum;
+    int64_t cinc = cost;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int u = __shfl_up(inc, d, 64);
+      const int64_t w = __shfl_up(cinc, d, 64);
+      if (lane >= d) {
+        inc += u;
+        cinc += w;
+      }
+    }
+    if (lane == 63) {
+      s_wsum[wave] = inc;
+      s_wcost[wave] = cinc;
+    }
+    if (tid <= kXcds) s_share[tid] = 0;
     __syncthreads();
-    int base = inc - sum;
-    for (int w = 0; w < wave; ++w) base += s_wsum[w];
+    int base = inc - sum, total = 0;
+    int64_t cbase = cinc - cost, ctotal = 0;
+    for (int w = 0; w < WM * WN; ++w) {
+      if (w < wave) {
+        base += s_wsum[w];
+        cbase += s_wcost[w];
+      }
+      total += s_wsum[w];
+      ctotal += s_wcost[w];
+    }
     for (int e = e0; e < e1; ++e) {
       segment(g.offsets, g.R, e, lo, hi);
-      s_start[e] = base;
-      base += div_up(hi - lo, BM);
+      const int tiles = MODE == kDw ? ntk : div_up(hi - lo, BM);
+      const int64_t c = cost_of(hi - lo, tiles);
+      if constexpr (MODE != kDw) s_start[e] = base;
+      for (int q = 1; q < kXcds; ++q) {  // the shares that end inside this expert
+        const int64_t at = ctotal * q / kXcds;
+        if (at >= cbase && at < cbase + c)
+          s_share[q] = base * per_tile + (int)((at - cbase) * tiles * per_tile / c);
+      }
+      base += tiles;
+      cbase += c;
     }
-    if (tid == NT - 1) s_start[g.E] = base;
+    if (tid == NT - 1) {
+      if constexpr (MODE != kDw) s_start[g.E] = total;
+      s_share[kXcds] = total * per_tile;
+    }
     __syncthreads();
-    total = __builtin_amdgcn_readfirstlane(s_start[g.E]) * per_tile;
   }
-  auto share = [&](int q) MOE_INLINE { return (int)((int64_t)total * q / kXcds); };
   auto find = [&](int item) MOE_INLINE {
     Item t;
     int tiles, local, beg, end;  // of the expert: M tiles, the item's place, the rows
@@ -169,7 +208,12 @@ void tile_kernel(const GroupedArgs g) {
                  __builtin_amdgcn_readfirstlane(tok_lds + tok_par * 256));
   };
   auto token = [&](int i, int tid) MOE_INLINE {
-    return *(MOE_LDS const int*)(uintptr_t)(tok_lds + tok_par * 256 + A::row_of(tid, i) * 4);
+    return *(MOE_LDS const uint32_t*)(uintptr_t)(tok_lds + tok_par * 256 + A::row_of(tid, i) * 4);
+  };
+  auto token_row = [&](uint32_t tk, int i) MOE_INLINE {  // (without branches: see the stage loop)
+    const bool named = tk < (uint32_t)g.T;
+    const char* p = a_base + a.off[i % A::kKinds] + (uint64_t)(named ? tk : 0) * (uint32_t)a_ld;
+    return named ? p : zeros;
   };
   auto setup = [&](const Item& t, int tid) MOE_INLINE {
     if constexpr (AMODE == kRows)
@@ -199,8 +243,9 @@ void tile_kernel(const GroupedArgs g) {
       load_tokens();
     }
   };
-  // Piece i of a whole stage (A's loads, then B's) into the slot at LDS address la.
-  auto copy_piece = [&](uint32_t la, int i) MOE_INLINE {
+  // Piece i of a whole stage (A's loads, then B's) into the slot at LDS address la (tk: dw with a
+  // gather, the piece's token).
+  auto copy_piece = [&](uint32_t la, int i, uint32_t tk) MOE_INLINE {
     if (i >= A::kLoads) {
       i -= A::kLoads;
       copy_to_lds(b.base_of(b_base, i, b_ld), b.off_of(i, (uint32_t)b_ld),
@@ -209,9 +254,7 @@ void tile_kernel(const GroupedArgs g) {
       copy_to_lds(a_ptr[i], la + i * NT * 16);
       a_ptr[i] += a_step;
     } else if constexpr (MODE == kDw && GATHER) {
-      const int tk = token(i, tid);
-      copy_to_lds((unsigned)tk < (unsigned)g.T ? a_base + tk * a_ld + a.off[i % A::kKinds] : zeros,
-                  la + i * NT * 16);
+      copy_to_lds(token_row(tk, i), la + i * NT * 16);
     } else {
       copy_to_lds(a.base_of(a_base, i, a_ld), a.off_of(i, (uint32_t)a_ld), la + i * NT * 16);
     }
@@ -228,10 +271,9 @@ void tile_kernel(const GroupedArgs g) {
     } else {
       if constexpr (MODE == kLinear && GATHER)
         src = a_ptr[i];
-      else if constexpr (MODE == kDw && GATHER) {
-        const int tk = token(i, tid);
-        src = (unsigned)tk < (unsigned)g.T ? a_base + tk * a_ld + a.off[i % A::kKinds] : zeros;
-      } else
+      else if constexpr (MODE == kDw && GATHER)
+        src = token_row(token(i, tid), i);
+      else
         src = a.base_of(a_base, i, a_ld) + a.off_of(i, (uint32_t)a_ld);
       at = AMODE == kRows ? A::piece_of(tid, i) * 8 : A::row_of(tid, i);
       la += i * NT * 16;
@@ -256,7 +298,8 @@ void tile_kernel(const GroupedArgs g) {
   // The copies run two stages ahead of the arithmetic, through this block's items in order: the
   // item being copied, what remains of its reduction (at least 1: an empty one is a stage of
   // zeros), the live length of its partial stage and its fragment count.
-  const int first = share(xcd) + (int)blockIdx.x / kXcds, last = share(xcd + 1);
+  const int first = __builtin_amdgcn_readfirstlane(s_share[xcd]) + (int)blockIdx.x / kXcds;
+  const int last = __builtin_amdgcn_readfirstlane(s_share[xcd + 1]);
   int cp_idx = first, cp_left = 0, cp_tail = 0, cp_nm = FM;
   auto frags_of = [&](int rows) MOE_INLINE {  // fragments that are computed: quarters of FM
     return max(1, div_up(rows, BM / 4)) * (FM / 4);
@@ -288,7 +331,8 @@ void tile_kernel(const GroupedArgs g) {
     if (cp_left >= kStage) {
 #pragma unroll
       for (int i = 0; i < A::kLoads + B::kLoads; ++i)
-        if (i < na || i >= A::kLoads) copy_piece(la, i);
+        if (i < na || i >= A::kLoads)
+          copy_piece(la, i, MODE == kDw && GATHER && i < A::kLoads ? token(i, tid) : 0);
     } else {
       int tid_v = tid;
       asm volatile("" : "+v"(tid_v));
@@ -355,13 +399,23 @@ void tile_kernel(const GroupedArgs g) {
     constexpr int NA = AMODE == kRows ? (A::kLoads * NM + FM - 1) / FM : A::kLoads, NC = NA + B::kLoads;
     const uint32_t so = (slot ^ 1) * kSlot;
     const uint32_t la = slot_lds(slot);
+    constexpr bool kTokens = MODE == kDw && GATHER && decltype(copy_c)::value;
+    uint32_t tk[A::kLoads] = {};
+    if constexpr (kTokens) {
+#pragma unroll
+      for (int i = 0; i < A::kLoads; ++i) tk[i] = token(i, tid);
+    }
 #pragma unroll
     for (int m = 0; m < NM; ++m) {
       if constexpr (decltype(copy_c)::value) {
         constexpr int per = (NC + NM - 1) / NM;
 #pragma unroll
-        for (int q = m * per; q < (m + 1) * per && q < NC; ++q)
-          copy_piece(la, q < NA ? q : q - NA + A::kLoads);
+        for (int q = m * per; q < (m + 1) * per && q < NC; ++q) {
+          // with tokens B's loads first, so that they have arrived
+          const int i = kTokens ? (q < B::kLoads ? A::kLoads + q : q - B::kLoads)
+                                : (q < NA ? q : q - NA + A::kLoads);
+          copy_piece(la, i, tk[i < A::kLoads ? i : 0]);
+        }
       }
       mfma_row(m, a1[m], b1);
       if (m == 0) {
@@ -598,31 +652,53 @@ void tile_kernel(const GroupedArgs g) {
   }
 }
 
-// db[e][n]: a block per expert and 64 columns; 32 row lanes of 8 threads (8 columns each) take
-// the rows in turn and are added up in order.
-__global__ __launch_bounds__(256) void dbias_kernel(const GroupedArgs g) {
-  __shared__ float part[32][64 + 1];
+// db[e][n], or a part's sums of it: a block per expert, 64 columns and part of the rows; 8 threads
+// of 8 columns each take a row, 128 rows at a time, 4 of them in flight per thread; the
+// threads' sums are added in order.
+__global__ __launch_bounds__(1024) void dbias_kernel(const GroupedArgs g, float* part) {
+  __shared__ float sums[128][64 + 1];
   const int e = blockIdx.y, c = threadIdx.x % 8 * 8, rl = threadIdx.x / 8;
   const int n = blockIdx.x * 64 + c;
   int lo, hi;
   segment(g.offsets, g.R, e, lo, hi);
+  const int len = hi - lo;
+  hi = lo + (int)((int64_t)len * (blockIdx.z + 1) / gridDim.z);
+  lo += (int)((int64_t)len * blockIdx.z / gridDim.z);
   float s[8] = {};
   if (n < g.N)
-    for (int r = lo + rl; r < hi; r += 32) {
-      float f[8];
-      unpack8(*(const uint4*)(g.w + (size_t)r * g.N + n), f);
+    for (int r = lo + rl; r < hi; r += 4 * 128) {
+      uint4 v[4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) s[i] += f[i];
+      for (int q = 0; q < 4; ++q) {
+        v[q] = make_uint4(0, 0, 0, 0);
+        if (r + q * 128 < hi) v[q] = *(const uint4*)(g.w + (size_t)(r + q * 128) * g.N + n);
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        float f[8];
+        unpack8(v[q], f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[i] += f[i];
+      }
     }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) part[rl][c + i] = s[i];
+  for (int i = 0; i < 8; ++i) sums[rl][c + i] = s[i];
   __syncthreads();
-  const int col = blockIdx.x * 64 + threadIdx.x;
-  if (threadIdx.x >= 64 || col >= g.N) return;
+  // 16 threads per column, 8 rows each, then their 16 sums
+  const int col = threadIdx.x & 63, k = threadIdx.x >> 6;
   float v = 0.0f;
-  for (int r = 0; r < 32; ++r) v += part[r][threadIdx.x];
-  float* d = g.dbias + (size_t)e * g.N + col;
-  *d = g.accumulate ? *d + v : v;
+  for (int r = 8 * k; r < 8 * k + 8; ++r) v += sums[r][col];
+  __syncthreads();
+  sums[k][col] = v;
+  __syncthreads();
+  if (k > 0 || blockIdx.x * 64 + col >= g.N) return;
+  v = 0.0f;
+  for (int r = 0; r < 16; ++r) v += sums[r][col];
+  const size_t o = (size_t)e * g.N + blockIdx.x * 64 + col;
+  if (part)
+    part[(size_t)blockIdx.z * g.E * g.N + o] = v;
+  else
+    g.dbias[o] = g.accumulate ? g.dbias[o] + v : v;
 }
 
 // 8 columns per thread: bound by memory, 7 bytes per value with a.
@@ -679,13 +755,18 @@ __global__ __launch_bounds__(256) void join_kernel(const GroupedArgs g) {
   finish4<MODE>(g, e, r, c, live, v);
 }
 
-// dw = the parts of a split weight gradient, added in order.
-__global__ __launch_bounds__(256) void join_dw_kernel(const GroupedArgs g, int64_t n4) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= n4) return;
-  f32x4_t* const o = (f32x4_t*)g.dw + i;
+// dw and dbias = the parts of a split weight gradient, added in order (n4, nb4: groups of 4).
+__global__ __launch_bounds__(256) void join_dw_kernel(const GroupedArgs g, int64_t n4, int64_t nb4,
+                                                      const float* bias_part) {
+  int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const bool bias = i >= n4;
+  if (bias) i -= n4;
+  if (bias && i >= nb4) return;
+  const int64_t n = bias ? nb4 : n4;
+  const f32x4_t* const part = (const f32x4_t*)(bias ? bias_part : g.part) + i;
+  f32x4_t* const o = (f32x4_t*)(bias ? g.dbias : g.dw) + i;
   f32x4_t v = g.accumulate ? *o : f32x4_t{};
-  for (int p = 0; p < g.split; ++p) v += *((const f32x4_t*)g.part + p * n4 + i);
+  for (int p = 0; p < g.split; ++p) v += part[p * n];
   *o = v;
 }
 
@@ -717,6 +798,11 @@ hipError_t run_grouped(const moe_grouped& p, GroupedArgs g, int mode, void* ws, 
   const GroupedPlan plan = grouped_plan(p, mode);
   g.split = plan.split;
   g.part = plan.split > 1 ? static_cast<float*>(ws) : nullptr;
+  float* const bias_part =
+      plan.split > 1 && mode == kDw ? g.part + (size_t)plan.split * g.E * g.K * g.N : nullptr;
+  if (mode == kDw && g.dbias)
+    hipLaunchKernelGGL(dbias_kernel, dim3(div_up(p.N, 64), p.E, plan.split), dim3(1024), 0, s, g,
+                       bias_part);
   if (plan.kernel == kStream) {
     const hipError_t err = launch_grouped_stream(g, mode, s);
     if (err != hipSuccess) return err;
@@ -732,7 +818,9 @@ hipError_t run_grouped(const moe_grouped& p, GroupedArgs g, int mode, void* ws, 
   if (plan.split > 1) {
     if (mode == kDw) {
       const int64_t n4 = (int64_t)g.E * g.K * g.N / 4;
-      hipLaunchKernelGGL(join_dw_kernel, dim3((unsigned)div_up64(n4, 256)), dim3(256), 0, s, g, n4);
+      const int64_t nb4 = g.dbias ? (int64_t)g.E * g.N / 4 : 0;
+      hipLaunchKernelGGL(join_dw_kernel, dim3((unsigned)div_up64(n4 + nb4, 256)), dim3(256), 0, s,
+                         g, n4, nb4, bias_part);
     } else {
       const int64_t n = (int64_t)g.R * div_up(mode == kDx ? g.K : g.N, 32) * 8;
       const dim3 grid((unsigned)div_up64(n, 256));
@@ -791,7 +879,8 @@ GroupedPlan grouped_plan(const moe_grouped& p, int mode) {
   }
   if (plan.split > 1)
     plan.ws_bytes = align256((size_t)plan.split * 4 *
-                             (mode == kDw ? (size_t)p.E * p.K * p.N : (size_t)p.R * ncols));
+                             (mode == kDw ? (size_t)p.E * (p.K + 1) * p.N  // and dbias's
+                                           : (size_t)p.R * ncols));
   return plan;
 }
 
@@ -821,8 +910,6 @@ hipError_t launch_grouped_dw(const moe_grouped& p, const void* x, const int32_t*
   GroupedArgs g{(const uint16_t*)x, (const uint16_t*)dz, row_token, offsets, nullptr, nullptr,
                 nullptr, nullptr, nullptr, nullptr, dw, dbias, p.R, p.T, p.K, p.N, p.E, 0,
                 accumulate, 1, nullptr};
-  if (dbias)
-    hipLaunchKernelGGL(dbias_kernel, dim3(div_up(p.N, 64), p.E), dim3(256), 0, s, g);
   return run_grouped(p, g, kDw, ws, s);
 }
 
