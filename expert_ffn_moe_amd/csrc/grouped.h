@@ -44,14 +44,21 @@ enum OperandMode { kRows = 0, kCols = 1 };
 // Source of the pieces outside an operand: 16 zero bytes, valid for every lane.
 __device__ __align__(16) const uint32_t g_zeros[4] = {0, 0, 0, 0};
 
-// 16 bytes per lane from base + off (base uniform), or from a lane's own address, to the
-// wavefront's 1 KiB at lds (uniform), lane by lane.  m0 carries the LDS address; one wait state
-// is required after writing it.
+// 16 bytes per lane from base + off (base uniform; ONCE: with the non-temporal hint), or from a
+// lane's own address, to the wavefront's 1 KiB at lds (uniform), lane by lane.  m0 carries the
+// LDS address; one wait state is required after writing it.
+template <bool ONCE = false>
 __device__ __forceinline__ void copy_to_lds(const char* base, uint32_t off, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
-               :
-               : "v"(off), "s"(base), "s"(lds)
-               : "memory");
+  if constexpr (ONCE)
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1 nt"
+                 :
+                 : "v"(off), "s"(base), "s"(lds)
+                 : "memory");
+  else
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
+                 :
+                 : "v"(off), "s"(base), "s"(lds)
+                 : "memory");
 }
 __device__ __forceinline__ void copy_to_lds(const char* src, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off"
@@ -200,7 +207,7 @@ __device__ __forceinline__ void segment(const int32_t* offsets, int R, int e, in
 enum GroupedMode { kLinear = 0, kDx = 1, kDw = 2 };
 
 // Which kernel a call takes, chosen from its sizes alone (the row counts are on the device).
-enum GroupedKernel { kStream = 0, kTile256, kTile128, kTile64 };
+enum GroupedKernel { kStream = 0, kTile256, kTile128, kTile64, kTile128Once };
 struct GroupedPlan {
   GroupedKernel kernel;
   int split;        // parts of the reduction

@@ -40,7 +40,8 @@ __device__ __forceinline__ void meet() { asm volatile(""); }
 // innermost, and cut into 8 shares of equal cost, one per XCD (workgroups go to XCDs
 // round-robin); a block takes every n-th item of its XCD's share, so that the operand bytes that
 // neighbouring items share (8 x 4 tiles at a time of a dense product) come from that XCD's L2.
-template <int MODE, bool GATHER, int BM, int BN, int WM, int WN>
+// ONCE: the weights are read once (one M tile per expert), with the non-temporal hint.
+template <int MODE, bool GATHER, int BM, int BN, int WM, int WN, bool ONCE = false>
 __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2, 2)))
 void tile_kernel(const GroupedArgs g) {
   constexpr int NT = 64 * WM * WN;
@@ -248,8 +249,8 @@ void tile_kernel(const GroupedArgs g) {
   auto copy_piece = [&](uint32_t la, int i, uint32_t tk) MOE_INLINE {
     if (i >= A::kLoads) {
       i -= A::kLoads;
-      copy_to_lds(b.base_of(b_base, i, b_ld), b.off_of(i, (uint32_t)b_ld),
-                  la + A::kBytes + i * NT * 16);
+      copy_to_lds<ONCE>(b.base_of(b_base, i, b_ld), b.off_of(i, (uint32_t)b_ld),
+                        la + A::kBytes + i * NT * 16);
     } else if constexpr (MODE == kLinear && GATHER) {
       copy_to_lds(a_ptr[i], la + i * NT * 16);
       a_ptr[i] += a_step;
@@ -789,6 +790,9 @@ void launch_tiles(const GroupedArgs& g, GroupedKernel kernel, hipStream_t s) {
   else if (kernel == kTile128)
     hipLaunchKernelGGL((tile_kernel<MODE, GATHER, 128, 128, 2, 2>), dim3(2 * cu_count()),
                        dim3(256), 0, s, g);
+  else if (MODE != kDw && kernel == kTile128Once)
+    hipLaunchKernelGGL((tile_kernel<MODE, GATHER, 128, 128, 2, 2, MODE != kDw>),
+                       dim3(2 * cu_count()), dim3(256), 0, s, g);
   else
     hipLaunchKernelGGL((tile_kernel<MODE, GATHER, 64, 128, 1, 4>), dim3(3 * cu_count()), dim3(256),
                        0, s, g);
@@ -872,7 +876,9 @@ GroupedPlan grouped_plan(const moe_grouped& p, int mode) {
   } else if (n128 >= 384) {
     // (4000 x 2048 x 2048: 41 us, 52 us with 64-tiles; 1003 x 1416 x 2056, 136 tiles: 26 us and
     // 22 us)
-    plan.kernel = kTile128;
+    // (4 rows for each of 256 experts, 7168 -> 2048: 1289 us, with the non-temporal hint 1167 us;
+    // 100 rows for each of 128, 2048 -> 768: 116 us and 107 us)
+    plan.kernel = rows <= 96 ? kTile128Once : kTile128;
   } else {
     // few tiles: long reductions in parts (100 x 7168 x 1024: 36 -> 16 us)
     plan.split = parts(red / 1024, 256 / n64);
@@ -907,6 +913,7 @@ hipError_t launch_grouped_dx(const moe_grouped& p, const void* dz, const int32_t
 hipError_t launch_grouped_dw(const moe_grouped& p, const void* x, const int32_t* row_token,
                              const void* dz, const int32_t* offsets, int accumulate, float* dw,
                              float* dbias, void* ws, hipStream_t s) {
+  if (p.R == 0) row_token = nullptr;  // no rows: only zeros to store, no list to read
   GroupedArgs g{(const uint16_t*)x, (const uint16_t*)dz, row_token, offsets, nullptr, nullptr,
                 nullptr, nullptr, nullptr, nullptr, dw, dbias, p.R, p.T, p.K, p.N, p.E, 0,
                 accumulate, 1, nullptr};

@@ -272,6 +272,15 @@ def test_no_rows_at_all():
     dw, db = m.grouped_linear_dw(p, e, dz, off, want_bias=True)
     torch.cuda.synchronize()
     assert not dw.any() and not db.any()
+    dw.fill_(3.0)
+    rt = torch.empty(0, dtype=torch.int32, device=DEV)
+    m.grouped_linear_dw(p, e, dz, off, row_token=rt, dw=dw)
+    torch.cuda.synchronize()
+    assert not dw.any()
+    dw.fill_(3.0)
+    m.grouped_linear_dw(p, e, dz, off, dw=dw, accumulate=True)
+    torch.cuda.synchronize()
+    assert bool((dw == 3.0).all())
     ck = m.checkpoint_buffers(0, 96)
     assert m.activation_backward(dz, ck, "silu").shape == (0, 96)
 
