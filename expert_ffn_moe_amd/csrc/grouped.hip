@@ -54,7 +54,7 @@ void tile_kernel(const GroupedArgs g) {
   __shared__ __align__(1024) char smem[2 * kSlot];
   __shared__ int s_start[MODE == kDw ? 1 : kMaxE + 1];  // linear, dx: M tiles before each expert
   __shared__ int s_wsum[WM * WN];
-  __shared__ int64_t s_wcost[WM * WN];
+  __shared__ int s_wcost[WM * WN];
   __shared__ int s_share[kXcds + 1];  // first item of each XCD's share
   __shared__ __align__(128) char s_stage[WM * WN * 2048];  // the epilogue's, see there
   __shared__ int s_tok[MODE == kDw && GATHER ? WM * WN * 128 : 1];
@@ -70,40 +70,38 @@ void tile_kernel(const GroupedArgs g) {
   // they cost, in rows (linear, dx: a tile's own time is that of 3/4 of its height more than its
   // rows') or stages (dw: storing a tile takes about 6) of an expert's items
   const int xcd = blockIdx.x % kXcds, slots = gridDim.x / kXcds;
-  {
+  const bool one = g.E == 1;  // nothing to look up: small dense calls start sooner
+  int first, last, beg1 = 0, end1 = 0;
+  if (one) {
+    segment(g.offsets, g.R, 0, beg1, end1);
+    beg1 = __builtin_amdgcn_readfirstlane(beg1);
+    end1 = __builtin_amdgcn_readfirstlane(end1);
+    const int total = (MODE == kDw ? div_up(g.K, BM) : div_up(end1 - beg1, BM)) * per_tile;
+    first = (int)((int64_t)total * xcd / kXcds);
+    last = (int)((int64_t)total * (xcd + 1) / kXcds);
+  } else {
     const int ntk = div_up(g.K, BM);
+    // (at most 2^30 rows and three quarters more)
     auto cost_of = [&](int len, int tiles) MOE_INLINE {
-      return MODE == kDw ? (int64_t)(div_up(len, kStage) + 6) : (int64_t)len + tiles * (BM * 3 / 4);
+      return MODE == kDw ? div_up(len, kStage) + 6 : len + tiles * (BM * 3 / 4);
     };
     const int per = div_up(g.E, NT);
     const int e0 = min(g.E, tid * per), e1 = min(g.E, e0 + per);
-    int sum = 0, lo, hi;
-    int64_t cost = 0;
+    int sum = 0, cost = 0, lo = 0, hi = 0;
     for (int e = e0; e < e1; ++e) {
       segment(g.offsets, g.R, e, lo, hi);
       const int tiles = MODE == kDw ? ntk : div_up(hi - lo, BM);
       sum += tiles;
       cost += cost_of(hi - lo, tiles);
     }
-    int inc = sum;
-    int64_t cinc = cost;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int u = __shfl_up(inc, d, 64);
-      const int64_t w = __shfl_up(cinc, d, 64);
-      if (lane >= d) {
-        inc += u;
-        cinc += w;
-      }
-    }
+    const int inc = wave_inclusive_scan(sum), cinc = wave_inclusive_scan(cost);
     if (lane == 63) {
       s_wsum[wave] = inc;
       s_wcost[wave] = cinc;
     }
     if (tid <= kXcds) s_share[tid] = 0;
     __syncthreads();
-    int base = inc - sum, total = 0;
-    int64_t cbase = cinc - cost, ctotal = 0;
+    int base = inc - sum, total = 0, cbase = cinc - cost, ctotal = 0;
     for (int w = 0; w < WM * WN; ++w) {
       if (w < wave) {
         base += s_wsum[w];
@@ -113,14 +111,14 @@ void tile_kernel(const GroupedArgs g) {
       ctotal += s_wcost[w];
     }
     for (int e = e0; e < e1; ++e) {
-      segment(g.offsets, g.R, e, lo, hi);
+      if (per > 1) segment(g.offsets, g.R, e, lo, hi);
       const int tiles = MODE == kDw ? ntk : div_up(hi - lo, BM);
-      const int64_t c = cost_of(hi - lo, tiles);
+      const int c = cost_of(hi - lo, tiles);
       if constexpr (MODE != kDw) s_start[e] = base;
       for (int q = 1; q < kXcds; ++q) {  // the shares that end inside this expert
-        const int64_t at = ctotal * q / kXcds;
+        const int at = (int)((int64_t)ctotal * q / kXcds);
         if (at >= cbase && at < cbase + c)
-          s_share[q] = base * per_tile + (int)((at - cbase) * tiles * per_tile / c);
+          s_share[q] = base * per_tile + (int)((int64_t)(at - cbase) * (tiles * per_tile) / c);
       }
       base += tiles;
       cbase += c;
@@ -130,11 +128,18 @@ void tile_kernel(const GroupedArgs g) {
       s_share[kXcds] = total * per_tile;
     }
     __syncthreads();
+    first = __builtin_amdgcn_readfirstlane(s_share[xcd]);
+    last = __builtin_amdgcn_readfirstlane(s_share[xcd + 1]);
   }
+  first += (int)blockIdx.x / kXcds;
   auto find = [&](int item) MOE_INLINE {
     Item t;
     int tiles, local, beg, end;  // of the expert: M tiles, the item's place, the rows
-    if constexpr (MODE == kDw) {
+    if (one) {
+      tiles = MODE == kDw ? div_up(g.K, BM) : div_up(end1 - beg1, BM);
+      t.e = 0;
+      local = item;
+    } else if constexpr (MODE == kDw) {
       tiles = div_up(g.K, BM);
       t.e = item / (tiles * per_tile);
       local = item - t.e * tiles * per_tile;
@@ -150,7 +155,12 @@ void tile_kernel(const GroupedArgs g) {
       tiles = start(lo + 1) - start(lo);
       local = item - per_tile * start(lo);
     }
-    segment(g.offsets, g.R, t.e, beg, end);
+    if (one) {
+      beg = beg1;
+      end = end1;
+    } else {
+      segment(g.offsets, g.R, t.e, beg, end);
+    }
     // a weight gradient over few rows is its output: tile after tile of the same rows of dW
     const int grouped = MODE == kDw && end - beg < 4096 ? 1 : 8;
     const int group = local / (grouped * per_tile) * grouped;
@@ -299,8 +309,6 @@ void tile_kernel(const GroupedArgs g) {
   // The copies run two stages ahead of the arithmetic, through this block's items in order: the
   // item being copied, what remains of its reduction (at least 1: an empty one is a stage of
   // zeros), the live length of its partial stage and its fragment count.
-  const int first = __builtin_amdgcn_readfirstlane(s_share[xcd]) + (int)blockIdx.x / kXcds;
-  const int last = __builtin_amdgcn_readfirstlane(s_share[xcd + 1]);
   int cp_idx = first, cp_left = 0, cp_tail = 0, cp_nm = FM;
   auto frags_of = [&](int rows) MOE_INLINE {  // fragments that are computed: quarters of FM
     return max(1, div_up(rows, BM / 4)) * (FM / 4);

@@ -27,7 +27,7 @@ __device__ __forceinline__ void wait_vm() {
 }
 
 template <int MODE, bool GATHER>
-__global__ __launch_bounds__(256) void stream_kernel(const GroupedArgs g) {
+__global__ __launch_bounds__(64 * kWaveParts) void stream_kernel(const GroupedArgs g) {
   constexpr int kStepBytes = MODE == kLinear ? 4096 + kStreamRows * 64 : 0;
   constexpr int kRingBytes = kWaveParts * kRing * kStepBytes;
   constexpr int kPartBytes = kWaveParts * kStreamRows * kStreamCols * 4;
@@ -172,13 +172,11 @@ __global__ __launch_bounds__(256) void stream_kernel(const GroupedArgs g) {
         *(f32x4_t*)(part + wave * kTile + (m * 16 + (lane & 15)) * kStreamCols + n * 16 +
                     (lane >> 4) * 4) = acc[m][n];
     __syncthreads();
+    for (int i = tid; i < NM * 256; i += 64 * kWaveParts) {  // whole wavefronts
+      const int r = i >> 4, c = n0 + (i & 15) * 4;
+      f32x4_t v = *(const f32x4_t*)(part + i * 4);
 #pragma unroll
-    for (int m = 0; m < NM; ++m) {
-      const int r = m * 16 + (tid >> 4), c = n0 + (tid & 15) * 4;
-      f32x4_t v = *(const f32x4_t*)(part + r * kStreamCols + (tid & 15) * 4);
-#pragma unroll
-      for (int w = 1; w < kWaveParts; ++w)
-        v += *(const f32x4_t*)(part + w * kTile + r * kStreamCols + (tid & 15) * 4);
+      for (int w = 1; w < kWaveParts; ++w) v += *(const f32x4_t*)(part + w * kTile + i * 4);
       const bool in = r < nlive && c < ncols;
       if (g.split > 1) {  // the joining kernel adds the blocks' parts
         if (in) *(f32x4_t*)(g.part + ((size_t)blockIdx.z * g.R + m0 + r) * ncols + c) = v;
@@ -204,7 +202,7 @@ __global__ __launch_bounds__(256) void stream_kernel(const GroupedArgs g) {
 }  // namespace
 
 hipError_t launch_grouped_stream(const GroupedArgs& g, int mode, hipStream_t s) {
-  const dim3 grid(div_up(mode == kDx ? g.K : g.N, kStreamCols), g.E, g.split), block(256);
+  const dim3 grid(div_up(mode == kDx ? g.K : g.N, kStreamCols), g.E, g.split), block(64 * kWaveParts);
   if (mode == kDx)
     hipLaunchKernelGGL((stream_kernel<kDx, false>), grid, block, 0, s, g);
   else if (g.row_token)
