@@ -292,6 +292,101 @@ def test_accumulated_weight_gradients(counts, K, N):
     check_dw(c, accumulate=True)
 
 
+# Sizes that reach each kernel and each way of splitting the reduction, with rows that are
+# unevenly spread, widths that end inside a tile and a partial last stage.
+FULL = [1300, 0, 900, 2, 700]          # many rows per expert
+PART = [300, 299, 0, 511, 1, 640, 97, 400]
+SPARSE = [(37 * i) % 101 for i in range(64)]  # less than a tile's rows per expert
+LONE = [0] * 20 + [400] + [0] * 11     # few rows, all of them one expert's
+
+
+@pytest.mark.parametrize("counts,K,N", [
+    (FULL, 264, 6176), (FULL, 6176, 264), (PART, 264, 2208), (PART, 2208, 264), (SPARSE, 264, 800),
+    (SPARSE, 800, 264), (LONE, 1096, 544), (LONE, 544, 1096), ([1], 4104, 1056),
+    ([16], 4104, 1056), ([1], 1056, 4104), ([100], 4104, 1056), ([100], 1056, 4104)])
+def test_products_of_every_size(counts, K, N):
+    say(f"case {counts[:8]} K={K} N={N}")
+    c = Case(counts, K, N, extra=7, seed=K + len(counts))
+    check_linear(c, "silu", bias=True, residual=True, ckpt=N % 32 == 0)
+    check_dx(c, "gelu_tanh" if K % 32 == 0 else "none", ckpt=K % 32 == 0)
+    c = Case(counts, K, N, extra=7, seed=K + len(counts) + 1, tokens=333)
+    check_linear(c, "relu2", bias=True, ckpt=N % 32 == 0)
+
+
+@pytest.mark.parametrize("tokens", [None, 333])
+@pytest.mark.parametrize("counts,K,N", [
+    (PART, 1288, 1032), (PART, 520, 1032), (SPARSE, 136, 264), ([3000], 264, 136),
+    ([5, 9000], 136, 520)])
+def test_weight_gradients_of_every_size(counts, K, N, tokens):
+    say(f"case {counts[:8]} K={K} N={N} tokens={tokens}")
+    c = Case(counts, K, N, extra=7, seed=K + len(counts), tokens=tokens)
+    check_dw(c, bias=True)
+    check_dw(c, bias=True, accumulate=True)
+
+
+def test_rows_behind_four_gigabytes():
+    """Byte offsets past 32 bits in x (gathered), z's row buffers, the weights and their
+    gradients; every value of a buffer's first and last rows, or of its last expert."""
+    m = moe()
+    g = gen(77)
+
+    def big(*shape):  # one block repeated: random bits of that many values take too long
+        t = torch.empty(*shape, dtype=BF, device=DEV)
+        rows = t.view(-1, shape[-1])
+        block = rand(g, 1021, shape[-1])
+        for r in range(0, rows.shape[0], 1021):
+            rows[r:r + 1021] = block[:rows.shape[0] - r]
+        return t
+
+    say("x")  # 600001 x 4096: 4.9 GB
+    T, R, K, N = 600001, 300, 4096, 136
+    x, w = big(T, K), rand(g, 2, K, N, scale=K ** -0.5)
+    rt = torch.randint(T - 1000, T, (R,), generator=g, device=DEV, dtype=torch.int32)
+    dz = rand(g, R, N)
+    p = m.GroupedProblem(R=R, K=K, N=N, E=2, T=T)
+    off = offsets_of([170, 130])
+    y = m.grouped_linear(p, x, w, off, row_token=rt)
+    dw, _ = m.grouped_linear_dw(p, x, dz, off, row_token=rt)
+    for e, (lo, hi) in enumerate(((0, 170), (170, 300))):
+        xe, we, de = x[rt[lo:hi].long()].to(F64), w[e].to(F64), dz[lo:hi].to(F64)
+        ref = xe @ we
+        within("y", y[lo:hi], ref, stored(ref, sum_tol(K, xe.abs() @ we.abs())))
+        within("dw", dw[e], xe.T @ de, sum_tol(hi - lo, xe.abs().T @ de.abs()))
+    del x, y, dw
+    say("rows")  # the same height in the layout, and y of 4.9 GB
+    R, K, N = 600001, 64, 4096
+    x, w = rand(g, R, K), rand(g, 2, K, N, scale=K ** -0.5)
+    off = offsets_of([R - 600, 600])
+    p = m.GroupedProblem(R=R, K=K, N=N, E=2)
+    y = m.grouped_linear(p, x, w, off)
+    dx = m.grouped_linear_dx(p, y, w, off)
+    for e, rows in ((0, slice(0, 500)), (0, slice(R - 700, R - 600)), (1, slice(R - 600, R))):
+        xe, we, ye = x[rows].to(F64), w[e].to(F64), y[rows].to(F64)
+        ref = xe @ we
+        within("y", y[rows], ref, stored(ref, sum_tol(K, xe.abs() @ we.abs())))
+        ref = ye @ we.T
+        within("dx", dx[rows], ref, stored(ref, sum_tol(N, ye.abs() @ we.abs().T)))
+    del y, dx, x
+    say("weights")  # 136 x 4096 x 4608: 5.1 GB of weights, 10.3 GB of gradients
+    E, K, N = 136, 4096, 4608
+    w = big(E, K, N)
+    for rows in (5, 70):
+        off = offsets_of([rows] * E)
+        p = m.GroupedProblem(R=rows * E, K=K, N=N, E=E)
+        x, dz = rand(g, rows * E, K), rand(g, rows * E, N)
+        y = m.grouped_linear(p, x, w, off)
+        dx = m.grouped_linear_dx(p, dz, w, off)
+        dw, _ = m.grouped_linear_dw(p, x, dz, off)
+        for e in (0, E - 1):
+            s = slice(rows * e, rows * (e + 1))
+            xe, we, de = x[s].to(F64), w[e].to(F64), dz[s].to(F64)
+            ref = xe @ we
+            within("y", y[s], ref, stored(ref, sum_tol(K, xe.abs() @ we.abs())))
+            ref = de @ we.T
+            within("dx", dx[s], ref, stored(ref, sum_tol(N, de.abs() @ we.abs().T)))
+            within("dw", dw[e], xe.T @ de, sum_tol(rows, xe.abs().T @ de.abs()))
+
+
 @pytest.mark.parametrize("act", ["none", "relu", "relu2", "silu", "gelu_tanh"])
 @pytest.mark.parametrize("rows,cols", [(1, 32), (61, 768), (300, 1408), (7, 4128)])
 def test_activation_backward(act, rows, cols):
