@@ -35,6 +35,60 @@ struct Item {
 // scalars for divergent.
 __device__ __forceinline__ void meet() { asm volatile(""); }
 
+// db[e][n], or a part's sums of it: an item per expert, 64 columns and part of the rows.  8
+// threads of 8 columns each take a row, NT / 8 rows at a time, 4 of them in flight per thread;
+// the threads' sums are added in order.
+template <int NT>
+__device__ __forceinline__ void bias_sums(const GroupedArgs& g, float* sums) {
+  constexpr int kAt = NT / 8, kPitch = 64 + 1;
+  const int tid = threadIdx.x, c = tid % 8 * 8, rl = tid / 8;
+  const int blocks = div_up(g.N, 64), items = blocks * g.E * g.split;
+  float* const out = g.split > 1 ? g.part + (size_t)g.split * g.E * g.K * g.N : g.dbias;
+  for (int item = blockIdx.x; item < items; item += gridDim.x) {
+    const int q = item / blocks, n0 = (item - q * blocks) * 64;
+    const int part = q / g.E, e = q - part * g.E;
+    int lo, hi;
+    segment(g.offsets, g.R, e, lo, hi);
+    const int len = hi - lo;
+    hi = lo + (int)((int64_t)len * (part + 1) / g.split);
+    lo += (int)((int64_t)len * part / g.split);
+    float s[8] = {};
+    if (n0 + c < g.N)
+      for (int r = lo + rl; r < hi; r += 4 * kAt) {
+        uint4 v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          v[i] = make_uint4(0, 0, 0, 0);
+          if (r + i * kAt < hi) v[i] = *(const uint4*)(g.w + (size_t)(r + i * kAt) * g.N + n0 + c);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float f[8];
+          unpack8(v[i], f);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) s[k] += f[k];
+        }
+      }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sums[rl * kPitch + c + i] = s[i];
+    __syncthreads();
+    // NT / 64 threads per column, 8 rows each, then their sums
+    const int col = tid & 63, k = tid >> 6;
+    float v = 0.0f;
+    for (int r = 8 * k; r < 8 * k + 8; ++r) v += sums[r * kPitch + col];
+    __syncthreads();
+    sums[k * kPitch + col] = v;
+    __syncthreads();
+    if (k == 0 && n0 + col < g.N) {
+      v = 0.0f;
+      for (int r = 0; r < NT / 64; ++r) v += sums[r * kPitch + col];
+      float* const o = out + ((size_t)part * g.E + e) * g.N + n0 + col;
+      *o = g.split == 1 && g.accumulate ? *o + v : v;
+    }
+    __syncthreads();
+  }
+}
+
 // Persistent.  The items are ordered expert by expert, within an expert by groups of 8 M tiles,
 // within a group N tile by N tile (and part by part of a split reduction) with the M tiles
 // innermost, and cut into 8 shares of equal cost, one per XCD (workgroups go to XCDs
@@ -65,6 +119,12 @@ void tile_kernel(const GroupedArgs g) {
   const uint32_t lds0 = (uint32_t)(uintptr_t)(MOE_LDS char*)smem;
   const int ncols = MODE == kDx ? g.K : g.N;
   const int ntn = div_up(ncols, BN), per_tile = ntn * g.split;  // items per M tile
+
+  // ---- dw: the bias sums first (in a launch of their own a small call took 5 us more)
+  if constexpr (MODE == kDw) {
+    if (g.dbias) bias_sums<NT>(g, (float*)smem);
+    meet();
+  }
 
   // ---- the M tiles before each expert, and this XCD's share of the items: an eighth of what
   // they cost, in rows (linear, dx: a tile's own time is that of 3/4 of its height more than its
@@ -661,55 +721,6 @@ void tile_kernel(const GroupedArgs g) {
   }
 }
 
-// db[e][n], or a part's sums of it: a block per expert, 64 columns and part of the rows; 8 threads
-// of 8 columns each take a row, 128 rows at a time, 4 of them in flight per thread; the
-// threads' sums are added in order.
-__global__ __launch_bounds__(1024) void dbias_kernel(const GroupedArgs g, float* part) {
-  __shared__ float sums[128][64 + 1];
-  const int e = blockIdx.y, c = threadIdx.x % 8 * 8, rl = threadIdx.x / 8;
-  const int n = blockIdx.x * 64 + c;
-  int lo, hi;
-  segment(g.offsets, g.R, e, lo, hi);
-  const int len = hi - lo;
-  hi = lo + (int)((int64_t)len * (blockIdx.z + 1) / gridDim.z);
-  lo += (int)((int64_t)len * blockIdx.z / gridDim.z);
-  float s[8] = {};
-  if (n < g.N)
-    for (int r = lo + rl; r < hi; r += 4 * 128) {
-      uint4 v[4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        v[q] = make_uint4(0, 0, 0, 0);
-        if (r + q * 128 < hi) v[q] = *(const uint4*)(g.w + (size_t)(r + q * 128) * g.N + n);
-      }
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        float f[8];
-        unpack8(v[q], f);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) s[i] += f[i];
-      }
-    }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) sums[rl][c + i] = s[i];
-  __syncthreads();
-  // 16 threads per column, 8 rows each, then their 16 sums
-  const int col = threadIdx.x & 63, k = threadIdx.x >> 6;
-  float v = 0.0f;
-  for (int r = 8 * k; r < 8 * k + 8; ++r) v += sums[r][col];
-  __syncthreads();
-  sums[k][col] = v;
-  __syncthreads();
-  if (k > 0 || blockIdx.x * 64 + col >= g.N) return;
-  v = 0.0f;
-  for (int r = 0; r < 16; ++r) v += sums[r][col];
-  const size_t o = (size_t)e * g.N + blockIdx.x * 64 + col;
-  if (part)
-    part[(size_t)blockIdx.z * g.E * g.N + o] = v;
-  else
-    g.dbias[o] = g.accumulate ? g.dbias[o] + v : v;
-}
-
 // 8 columns per thread: bound by memory, 7 bytes per value with a.
 __global__ __launch_bounds__(256) void act_backward_kernel(
     int64_t n8, int cols8, const int32_t* __restrict__ live, int act,
@@ -812,9 +823,6 @@ hipError_t run_grouped(const moe_grouped& p, GroupedArgs g, int mode, void* ws, 
   g.part = plan.split > 1 ? static_cast<float*>(ws) : nullptr;
   float* const bias_part =
       plan.split > 1 && mode == kDw ? g.part + (size_t)plan.split * g.E * g.K * g.N : nullptr;
-  if (mode == kDw && g.dbias)
-    hipLaunchKernelGGL(dbias_kernel, dim3(div_up(p.N, 64), p.E, plan.split), dim3(1024), 0, s, g,
-                       bias_part);
   if (plan.kernel == kStream) {
     const hipError_t err = launch_grouped_stream(g, mode, s);
     if (err != hipSuccess) return err;
