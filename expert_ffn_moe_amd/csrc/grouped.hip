@@ -869,10 +869,11 @@ GroupedPlan grouped_plan(const moe_grouped& p, int mode) {
   if (mode == kDw) {
     // 256-tiles where they fill the chip (2048 x 768 x 128 experts: 192 us against 221 us with
     // 128-tiles); else over many rows 128-tiles and the rows split (one 2048 x 768 over 16384
-    // rows: 131 -> 65 us with 5 parts); over few rows the smallest that fill it
+    // rows: 131 -> 65 us with 5 parts; over 3000 rows 25 us, 64-tiles 28; over 1536 rows 21 us
+    // with 3 parts, 64-tiles 13); over fewer rows the smallest that fill it
     if (n256 >= 192) {
       plan.kernel = kTile256;
-    } else if (rows >= 1024) {
+    } else if (rows >= 2048) {
       plan.kernel = kTile128;
       plan.split = parts(rows / 512, 512 / n128);
     } else if (n128 >= 256) {
@@ -896,8 +897,9 @@ GroupedPlan grouped_plan(const moe_grouped& p, int mode) {
     // 100 rows for each of 128, 2048 -> 768: 116 us and 107 us)
     plan.kernel = rows <= 96 ? kTile128Once : kTile128;
   } else {
-    // few tiles: long reductions in parts (100 x 7168 x 1024: 36 -> 16 us)
-    plan.split = parts(red / 1024, 256 / n64);
+    // few tiles: long reductions in parts (100 x 7168 x 1024: 36 -> 16 us; 153 tiles of
+    // 1034 x 4096 x 1056: 38 us, 28 in 2 parts, 24 in 3; of 1034 x 1416 x 1056: 16 us, 18 in 2)
+    plan.split = parts(red / 1000, 512 / n64);
   }
   if (plan.split > 1)
     plan.ws_bytes = align256((size_t)plan.split * 4 *
