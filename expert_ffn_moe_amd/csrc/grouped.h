@@ -7,14 +7,16 @@
 // read, so that neither x, W nor dz is ever transposed or packed in memory:
 //   linear   x  kRows    W  kCols        dx   dz kRows   W  kRows        dw   x kCols   dz kCols
 //
-// Two LDS slots: a stage's copies are issued when the stage before starts to compute, one
-// barrier per stage.  The copies write lane-consecutive 16-byte pieces, so the bank swizzle
-// is made on the source side (which piece of its row a lane fetches):
+// Two LDS slots, one barrier per stage, in its middle: by then every wavefront holds the second
+// half's fragments in registers, and the copies of the stage after the next go into the slot
+// just read.  The copies write lane-consecutive 16-byte pieces, so the bank swizzle is made on
+// the source side (which piece of its row a lane fetches):
 //   kRows  piece c of row r sits at c ^ f(r), f(r) = ((r >> 1) ^ (r << 2)) & 7: 16 rows at one
 //          c cover all 64 banks;
 //   kCols  piece c of row k sits at c ^ 2 ((k & 3) | (k >> 3 & m) << 2), m = 3 (256 columns) or
-//          1 (128), for 64 columns 2 ((k >> 1 & 1) | (k >> 3 & 1) << 1): the 32-byte pairs that a transposing read takes from rows 8 g + 0 .. 3 of
-//          its four lane groups lie in different banks.
+//          1 (128), for 64 columns 2 ((k >> 1 & 1) | (k >> 3 & 1) << 1): the 32-byte pairs
+//          that a transposing read takes from rows 8 g + 0 .. 3 of its four lane groups lie in
+//          different banks.
 //
 // The copies are written as inline assembly (they have no register outputs) with explicit
 // waits: for the builtin form the compiler waits for every copy in flight before each LDS
