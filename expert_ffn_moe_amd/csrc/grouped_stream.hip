@@ -12,8 +12,9 @@
 // Measured: one token's 8 experts, 2048 -> 768 (25 MB of weights): 11.3 us, 2.2 TB/s, of which
 // the launch, the first copies and the sums through LDS are 4; 4 rows for each of 64 experts,
 // 4096 -> 1408 (738 MB): 129 us, 5.7 TB/s.  8 parts instead of 4: 0.5 us less for the one token, 5
-// to 13% more elsewhere.  An expert that holds many of the rows is taken 32 rows at a time, its
-// weights then coming from the caches.
+// to 13% more elsewhere.  An expert that holds many of the rows is taken 32 rows at a time by
+// up to 8 blocks per 64 columns (512 rows, all on one of 32 experts, 4096 -> 2048: 267 us with one
+// block, 49 us; with 128-tiles 48).
 #include <algorithm>
 
 #include "grouped.h"
@@ -40,13 +41,17 @@ __global__ __launch_bounds__(64 * kWaveParts) void stream_kernel(const GroupedAr
   const int e = blockIdx.y, n0 = blockIdx.x * kStreamCols;
   int lo, hi;
   segment(g.offsets, g.R, e, lo, hi);
-  if (lo >= hi) return;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int red = MODE == kLinear ? g.K : g.N, ncols = MODE == kDx ? g.K : g.N;
-  // this wavefront's part of this block's part (blockIdx.z) of the reduction
+  // blockIdx.z: this block's part of a split reduction, or else its place among the blocks that
+  // share an expert's rows
+  const int part_z = g.split > 1 ? blockIdx.z : 0;
+  const int row_z = g.split > 1 ? 0 : blockIdx.z, row_blocks = g.split > 1 ? 1 : gridDim.z;
+  if (lo + row_z * kStreamRows >= hi) return;
+  // this wavefront's part of this block's part of the reduction
   const int steps = div_up(red, 32), parts = kWaveParts * g.split;
-  const int mine = kWaveParts * blockIdx.z + wave;
+  const int mine = kWaveParts * part_z + wave;
   const int s0 = (int)((int64_t)steps * mine / parts);
   const int s1 = (int)((int64_t)steps * (mine + 1) / parts);
   const char* const zeros = reinterpret_cast<const char*>(g_zeros);
@@ -184,7 +189,7 @@ __global__ __launch_bounds__(64 * kWaveParts) void stream_kernel(const GroupedAr
       for (int w = 1; w < kWaveParts; ++w) v += *(const f32x4_t*)(part + w * kTile + i * 4);
       const bool in = r < nlive && c < ncols;
       if (g.split > 1) {  // the joining kernel adds the blocks' parts
-        if (in) *(f32x4_t*)(g.part + ((size_t)blockIdx.z * g.R + m0 + r) * ncols + c) = v;
+        if (in) *(f32x4_t*)(g.part + ((size_t)part_z * g.R + m0 + r) * ncols + c) = v;
         continue;
       }
       if constexpr (GATHER) {
@@ -195,7 +200,7 @@ __global__ __launch_bounds__(64 * kWaveParts) void stream_kernel(const GroupedAr
     }
     __syncthreads();  // before the next rows' copies
   };
-  for (int m0 = lo; m0 < hi; m0 += kStreamRows) {
+  for (int m0 = lo + row_z * kStreamRows; m0 < hi; m0 += row_blocks * kStreamRows) {
     const int n = min(kStreamRows, hi - m0);
     if (n > 16)
       rows(std::integral_constant<int, 2>{}, m0, n);
@@ -207,7 +212,12 @@ __global__ __launch_bounds__(64 * kWaveParts) void stream_kernel(const GroupedAr
 }  // namespace
 
 hipError_t launch_grouped_stream(const GroupedArgs& g, int mode, hipStream_t s) {
-  const dim3 grid(div_up(mode == kDx ? g.K : g.N, kStreamCols), g.E, g.split), block(64 * kWaveParts);
+  // an expert's rows beyond the first 32 go to blocks of their own, which end at once where it has
+  // no more (at most 8: later rounds find the weights in the caches)
+  const int row_blocks = std::max(1, std::min(8, g.R / (2 * kStreamRows)));
+  const dim3 grid(div_up(mode == kDx ? g.K : g.N, kStreamCols), g.E,
+                  g.split > 1 ? g.split : row_blocks);
+  const dim3 block(64 * kWaveParts);
   if (mode == kDx)
     hipLaunchKernelGGL((stream_kernel<kDx, false>), grid, block, 0, s, g);
   else if (g.row_token)
