@@ -14,6 +14,7 @@
 // of a 64-token chunk), every rank from a popcount of the bits below the token, every
 // sum from a fixed-order scan.  LDS atomics only set bits or count into a histogram,
 // whose results do not depend on their order.
+#include "grouped_launch.h"
 #include "moe_internal.h"
 #include "wave.h"
 

@@ -25,6 +25,7 @@
 #include <algorithm>
 
 #include "grouped.h"
+#include "grouped_launch.h"
 #include "moe_internal.h"
 #include "wave.h"
 

@@ -7,6 +7,7 @@
 #include <initializer_list>
 #include <mutex>
 
+#include "grouped_launch.h"
 #include "moe_internal.h"
 
 namespace moe {

@@ -85,10 +85,6 @@ hipError_t launch_capacity_select(const moe_problem& p, const int32_t* cand_coun
 // word; debug_status_take waits for the device, reads the word and clears it.
 hipError_t launch_check_ids(const moe_problem& p, const int32_t* ids, hipStream_t s);
 hipError_t debug_status_take(uint32_t* out);
-// Grouped products: offsets (if not NULL) non-decreasing inside [0, R], row_token (if not
-// NULL) of the rows they name inside [0, T).
-hipError_t launch_check_grouped(const moe_grouped& g, const int32_t* offsets,
-                                const int32_t* row_token, hipStream_t s);
 #endif
 // Row gather xp[slot_to_row[t, j]] = x[t].
 hipError_t launch_gather(const moe_problem& p, const void* x, const int32_t* slot_to_row,
@@ -184,22 +180,5 @@ hipError_t launch_gate_up_fp8(const moe_problem& p, const uint8_t* xq, const uin
 hipError_t launch_down_fp8(const moe_problem& p, const uint8_t* aq, const uint8_t* as,
                            const int32_t* offsets, const void* packed_d, void* yp,
                            hipStream_t s);
-
-// ---- grouped.hip (natural-layout grouped products; the arguments are those of the C entries)
-hipError_t launch_grouped_linear(const moe_grouped& g, const void* x, const int32_t* row_token,
-                                 const int32_t* offsets, const void* w, const void* bias, int act,
-                                 const void* residual, void* y, uint8_t* codes, uint8_t* scales,
-                                 void* ws, hipStream_t s);
-hipError_t launch_grouped_dx(const moe_grouped& g, const void* dz, const int32_t* offsets,
-                             const void* w, int act, const uint8_t* codes, const uint8_t* scales,
-                             void* dx, void* a, void* ws, hipStream_t s);
-hipError_t launch_grouped_dw(const moe_grouped& g, const void* x, const int32_t* row_token,
-                             const void* dz, const int32_t* offsets, int accumulate, float* dw,
-                             float* dbias, void* ws, hipStream_t s);
-// Workspace of a moe_grouped_op.
-size_t grouped_ws_bytes(const moe_grouped& g, int op);
-hipError_t launch_act_backward(int64_t rows, int cols, const int32_t* live, int act,
-                               const void* dy, const uint8_t* codes, const uint8_t* scales,
-                               void* dz, void* a, hipStream_t s);
 
 }  // namespace moe
