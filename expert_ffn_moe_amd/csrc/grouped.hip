@@ -740,11 +740,11 @@ void tile_kernel(const GroupedArgs g) {
 // 8 columns per thread: bound by memory, 7.03 bytes per value with a (18300 x 1408, 181 MB: 22 us,
 // 8.2 TB/s, part of it from the last-level cache).
 __global__ __launch_bounds__(256) void act_backward_kernel(
-    int64_t n8, int cols8, const int32_t* __restrict__ live, int act,
+    int64_t i0, int64_t n8, int cols8, const int32_t* __restrict__ live, int act,
     const uint4* __restrict__ dy, const uint2* __restrict__ codes,
     const uint8_t* __restrict__ scales, uint4* __restrict__ dz, uint4* __restrict__ a) {
   if (live) n8 = min(n8, (int64_t)max(*live, 0) * cols8);
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t i = i0 + (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (i >= n8) return;
   const uint2 q = codes[i];
   const int s = scales[i >> 2];
@@ -960,12 +960,19 @@ size_t grouped_ws_bytes(const moe_grouped& p, int op) { return grouped_plan(p, o
 hipError_t launch_act_backward(int64_t rows, int cols, const int32_t* live, int act,
                                const void* dy, const uint8_t* codes, const uint8_t* scales,
                                void* dz, void* a, hipStream_t s) {
+  // a launch holds fewer than 2^32 threads: 2^32 values at a time
+  constexpr int64_t kBlocks = 1 << 21;
+  static_assert(kBlocks * 256 < (int64_t)1 << 32, "");
   const int64_t n8 = rows * (cols / 8);
-  if (div_up64(n8, 256) > INT32_MAX) return hipErrorInvalidValue;  // (refused by the caller)
-  hipLaunchKernelGGL(act_backward_kernel, dim3((unsigned)div_up64(n8, 256)), dim3(256), 0, s, n8,
-                     cols / 8, live, act, (const uint4*)dy, (const uint2*)codes, scales,
-                     (uint4*)dz, (uint4*)a);
-  return hipGetLastError();
+  for (int64_t at = 0; at < n8; at += kBlocks * 256) {
+    const int64_t blocks = std::min(div_up64(n8 - at, 256), kBlocks);
+    hipLaunchKernelGGL(act_backward_kernel, dim3((unsigned)blocks), dim3(256), 0, s, at, n8,
+                       cols / 8, live, act, (const uint4*)dy, (const uint2*)codes, scales,
+                       (uint4*)dz, (uint4*)a);
+    const hipError_t err = hipGetLastError();
+    if (err != hipSuccess) return err;
+  }
+  return hipSuccess;
 }
 
 }  // namespace moe

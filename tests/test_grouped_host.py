@@ -154,3 +154,15 @@ def test_python_refusals():
         m.checkpoint_buffers(4, 40, device="cpu")
     with pytest.raises(ValueError, match="unknown activation"):
         m._act("gelu")
+
+
+def test_activation_backward_size_limit():
+    """rows * cols up to 2^39 is taken, one row more is refused; the stand-in pointers lie so far
+    apart that only the size can be the reason."""
+    m = moe()
+    dy, zc, zs, dz = fake(4, base=1 << 45)
+    far = [ctypes.c_void_p(p.value + (i << 43)) for i, p in enumerate((dy, zc, zs, dz))]
+    for cols in (32, 4096):
+        rows = (1 << 39) // cols + 1
+        st = m.lib.moe_activation_backward(rows, cols, None, 3, *far, None, None)
+        assert st == m.MOE_ERR_INVALID_ARG
