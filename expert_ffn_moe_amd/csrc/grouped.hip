@@ -281,14 +281,16 @@ void tile_kernel(const GroupedArgs g) {
   B b{};
   const char *a_base, *b_base;
   const char* a_ptr[MODE == kLinear && GATHER ? A::kLoads : 1];
-  int tok_row = 0, tok_par = 0;  // dw: first row of the next stage to be copied, its list's place
+  int tok_row = 0, tok_par = 0;  // dw: first row of the next stage to be copied, its list
   const char* const zeros = reinterpret_cast<const char*>(g_zeros);
   const size_t a_ld = 2 * (size_t)(MODE == kDx ? g.N : g.K);  // bytes of a row of A
   const size_t b_ld = 2 * (size_t)g.N;
   const size_t a_step = AMODE == kRows ? 2 * kStage : kStage * a_ld;
   const size_t b_step = BMODE == kRows ? 2 * kStage : kStage * b_ld;
   // dw with a gather: the tokens of the next stage's rows, as a copy to a list of this
-  // wavefront's own (two take turns), so that no register waits for them
+  // wavefront's own, so that no register waits for them.  Two lists take turns from copy to copy,
+  // through the items too: no copy goes to a list that another one in flight writes (behind an
+  // item's last whole stage next_stage has started one that nothing reads)
   const uint32_t tok_lds = (uint32_t)(uintptr_t)(MOE_LDS int*)s_tok + wave * 512;
   auto load_tokens = [&]() MOE_INLINE {
     copy4_to_lds(g.row_token + min(tok_row + (int)(threadIdx.x & 63), g.R - 1),
@@ -327,6 +329,7 @@ void tile_kernel(const GroupedArgs g) {
     b.set(tid, (uint32_t)b_ld, BMODE == kRows ? ncols - 1 - t.n0 : (ncols - t.n0) / 8 - 1);
     if constexpr (MODE == kDw && GATHER) {
       tok_row = t.k0;
+      tok_par ^= 1;
       load_tokens();
     }
   };
