@@ -212,6 +212,7 @@ __global__ __launch_bounds__(64 * kWaveParts) void stream_kernel(const GroupedAr
 }  // namespace
 
 hipError_t launch_grouped_stream(const GroupedArgs& g, int mode, hipStream_t s) {
+  if (mode != kLinear && mode != kDx) return hipErrorInvalidValue;  // no weight gradients here
   // an expert's rows beyond the first 32 go to blocks of their own, which end at once where it has
   // no more (at most 8: later rounds find the weights in the caches)
   const int row_blocks = std::max(1, std::min(8, g.R / (2 * kStreamRows)));
