@@ -588,6 +588,9 @@ class GroupedProblem:
         object.__setattr__(self, "_ref", ctypes.byref(c))
         object.__setattr__(self, "_ws_bytes", {})
 
+    def __reduce__(self):  # a copy derives its own: the C struct's reference cannot be copied
+        return type(self), (self.R, self.K, self.N, self.E, self.T)
+
     def c(self) -> MoeGrouped:
         return MoeGrouped(self.R, self.x_tokens, self.K, self.N, self.E)
 

@@ -1,6 +1,8 @@
 """Host-side checks of the grouped linear entry points: shapes, pointers, aliasing and
 workspaces are refused before anything is enqueued.  No kernel is launched here."""
+import copy
 import ctypes
+import pickle
 
 import pytest
 import torch
@@ -166,3 +168,17 @@ def test_activation_backward_size_limit():
         rows = (1 << 39) // cols + 1
         st = m.lib.moe_activation_backward(rows, cols, None, 3, *far, None, None)
         assert st == m.MOE_ERR_INVALID_ARG
+
+
+def test_problem_can_be_copied_and_pickled():
+    """As Problem can: a program's configuration goes to worker processes and into checkpoints."""
+    m = moe()
+    for p in (m.GroupedProblem(64, 128, 96, 4, 32), m.GroupedProblem(R=16, K=4096, N=4096)):
+        need = [p.workspace_bytes(op) for op in range(3)]  # derived state is there
+        for q in (pickle.loads(pickle.dumps(p)), copy.copy(p), copy.deepcopy(p)):
+            assert q == p and hash(q) == hash(p) and q.T == p.T
+            assert q.check() == m.MOE_OK
+            assert [q.workspace_bytes(op) for op in range(3)] == need
+            assert (q.c().R, q.c().T, q.c().K, q.c().N, q.c().E) == \
+                (p.R, p.x_tokens, p.K, p.N, p.E)
+            assert q._c is not p._c and q._ws_bytes is not p._ws_bytes
