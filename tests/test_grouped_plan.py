@@ -5,9 +5,8 @@ import ctypes
 import pytest
 
 from grouped_common import moe
-
-STREAM, TILE256, TILE128, TILE64, TILE128_ONCE = range(5)
-LINEAR, DX, DW = range(3)
+from grouped_paths import (DW, DX, LINEAR, PATHS, STREAM, TILE64, TILE128, TILE128_ONCE,
+                           TILE256)
 
 
 class Plan(ctypes.Structure):
@@ -43,3 +42,26 @@ def test_weight_gradients_never_stream():
         for K, N in ((8, 8), (64, 128), (520, 1096), (2048, 768), (7168, 2048)):
             for R in (0, 1, 8, 100, 4096, 131072, 1 << 24):
                 assert plan(R, K, N, E, DW)[0] in (TILE256, TILE128, TILE64), (E, K, N, R)
+
+
+@pytest.mark.parametrize("p", PATHS, ids=lambda p: p.name)
+def test_paths_reach_their_kernel(p):
+    assert plan(sum(p.counts) + p.extra, p.K, p.N, len(p.counts), p.mode) == (p.kernel, p.split)
+
+
+def test_paths_reach_every_kernel_and_split():
+    tiles = {(m, k, False) for m in (LINEAR, DX) for k in (STREAM, TILE256, TILE128, TILE64,
+                                                           TILE128_ONCE)}
+    parts = {(m, k, True) for m in (LINEAR, DX) for k in (STREAM, TILE64)}
+    dw = {(DW, TILE256, False), (DW, TILE128, False), (DW, TILE128, True), (DW, TILE64, False)}
+    assert {(p.mode, p.kernel, p.split > 1) for p in PATHS} == tiles | parts | dw
+    # and the choice knows no others
+    seen = set()
+    for mode in (LINEAR, DX, DW):
+        for E in (1, 2, 8, 60, 256, 1024):
+            for K in (8, 128, 520, 2048, 7168):
+                for N in (8, 128, 520, 2048, 7168):
+                    for R in (0, 1, 8, 100, 1000, 4096, 32768, 131072):
+                        kernel, split = plan(R, K, N, E, mode)
+                        seen.add((mode, kernel, split > 1))
+    assert seen <= tiles | parts | dw
