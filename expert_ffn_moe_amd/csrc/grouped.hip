@@ -18,9 +18,10 @@
 //     experts of 512 +- 22 rows with activation and checkpoint (their ragged tiles: 3 x 192 or
 //     2 x 256 rows per expert);
 //   - in between, the operands' way through L2 into LDS and the first and last stages of short
-//     items (256 rows for each of 128 experts, 2048 -> 768: 0.18 ms, 580 TFLOP/s);
-//   - weight gradients: fp32 stores (128 of 2048 x 768, 805 MB, in 0.27 ms), which the next
-//     item's first wait for copies also waits for;
+//     items (256 rows for each of 128 experts, 2048 -> 768: 0.18 ms, 570 TFLOP/s; counters: 1.81
+//     GB out of the L2 at 10.0 TB/s, the matrix cores busy 30% of the CUs' busy time);
+//   - weight gradients: fp32 stores (128 of 2048 x 768, 805 MB, in 0.26 to 0.28 ms, gathered and
+//     with bias sums), which the next item's first wait for copies also waits for;
 //   - small calls: the launch and the first copies, 6 us, and 0.27 us per stage of 64.
 #include <algorithm>
 
@@ -740,8 +741,9 @@ void tile_kernel(const GroupedArgs g) {
   }
 }
 
-// 8 columns per thread: bound by memory, 7.03 bytes per value with a (18300 x 1408, 181 MB: 22 us,
-// 8.2 TB/s, part of it from the last-level cache).
+// 8 columns per thread, from value 8 i0 on: bound by memory, 7.03 bytes per value with a (13400 x
+// 1408, 132 MB: 26.8 us a call on buffers that take turns, 4.9 TB/s, the rate of a large copy; 22 us
+// for the fastest of 8 on the same buffers, part of it from the last-level cache).
 __global__ __launch_bounds__(256) void act_backward_kernel(
     int64_t i0, int64_t n8, int cols8, const int32_t* __restrict__ live, int act,
     const uint4* __restrict__ dy, const uint2* __restrict__ codes,
@@ -832,7 +834,7 @@ void launch_tiles(const GroupedArgs& g, GroupedKernel kernel, hipStream_t s) {
   else if (MODE != kDw && kernel == kTile128Once)
     hipLaunchKernelGGL((tile_kernel<MODE, GATHER, 128, 128, 2, 2, MODE != kDw>),
                        dim3(2 * cu_count()), dim3(256), 0, s, g);
-  else
+  else  // (of three blocks per CU two are resident, 57 to 62 KB of LDS each; the others follow)
     hipLaunchKernelGGL((tile_kernel<MODE, GATHER, 64, 128, 1, 4>), dim3(3 * cu_count()), dim3(256),
                        0, s, g);
 }

@@ -9,8 +9,9 @@
 //           transposing LDS read; three steps deep, two blocks per CU: 120 KiB in flight.
 //   dx:     W's rows are the output columns and its columns the reduction, which is the order
 //           of the matrix instruction's operand: the weights go straight to registers.
-// Measured: one token's 8 experts, 2048 -> 768 (25 MB of weights): 11.3 us, 2.2 TB/s, of which
-// the launch, the first copies and the sums through LDS are 4; 4 rows for each of 64 experts,
+// Measured: one token's 8 experts, 2048 -> 768 (25 MB of weights): 12.5 us a call on buffers that
+// take turns, 2.0 TB/s (the kernel alone, 8 calls on the same weights: 10.6 us the fastest, 12.8 on
+// average), of which the launch, the first copies and the sums through LDS are 4; 4 rows for each of 64 experts,
 // 4096 -> 1408 (738 MB): 129 us, 5.7 TB/s.  8 parts instead of 4: 0.5 us less for the one token, 5
 // to 13% more elsewhere.  An expert that holds many of the rows is taken 32 rows at a time by
 // up to 8 blocks per 64 columns (512 rows, all on one of 32 experts, 4096 -> 2048: 267 us with one

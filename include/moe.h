@@ -445,13 +445,17 @@ int moe_layer_backward(const moe_problem* p, const void* x, const float* logits,
  * [E, K, N] (y = x W): nothing is packed, so weights that change every step can be used as
  * they are.  Rows are those of the prefix-sum layout: expert e owns rows offsets[e] ..
  * offsets[e + 1] - 1 (offsets from moe_dispatch).  offsets may be NULL when E = 1: all R rows
- * belong to the one expert.  Rows >= offsets[E] are neither read nor written.
+ * belong to the one expert.  Rows in front of offsets[0] and from offsets[E] on are neither read
+ * nor written.
  *
  * Everything is bf16 (fp32 accumulation, each stored bf16 value rounded once) except the
  * weight and bias gradients, which are fp32.  Every result is deterministic.  A sigmoid below
  * 2^-126 counts as zero.
  * The kernels take offsets as clamped to [0, R], and read zeros for a row whose row_token
  * lies outside [0, T); the debug library reports both (moe_debug_status bits 2 and 3).
+ * Decreasing offsets are the caller's error: their experts' rows overlap, and the kernels stay
+ * inside the buffers only while the tiles of all experts together stay below 2^31 (as they
+ * always do for offsets that do not decrease, see moe_grouped_check).
  *
  *   R     rows the row buffers hold (0: they may be NULL and nothing is enqueued, except that
  *         moe_grouped_linear_dw still clears its outputs)
