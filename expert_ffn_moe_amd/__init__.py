@@ -8,8 +8,9 @@ package raises -- there is no other implementation.
 
 Call names follow the C ABI: route, dispatch, expert_gate_up, expert_gate_up_gather,
 expert_down, expert_ffn, combine, layer, quantize_fp8, grouped_linear (with its gradients
-grouped_linear_dx, grouped_linear_dw and activation_backward), plus pack_weights for the
-one-time weight packing.
+grouped_linear_dx, grouped_linear_dw and activation_backward), route_scored, router_scored and
+route_scored_backward, quantize_fp4, dequantize_fp4, quantize_fp4_weights and
+grouped_linear_fp4, plus pack_weights for the one-time weight packing.
 
 Problem.dtype "fp8" means FP8 (E4M3, UE8M0 block scales) expert weights with bf16
 activations: pack_weights then takes bf16 weights and quantises them, and the intermediate
@@ -19,6 +20,7 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
+import functools
 import os
 from typing import Optional
 
@@ -28,11 +30,13 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmoe.so")
 
 MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_HIP = range(5)
-MOE_F32, MOE_BF16, MOE_FP8 = 0, 1, 2
+MOE_F32, MOE_BF16, MOE_FP8, MOE_FP4 = 0, 1, 2, 3
 QBLOCK = 32  # elements per UE8M0 scale
 OP_ROUTE, OP_DISPATCH, OP_FFN, OP_COMBINE, OP_LAYER, OP_ROUTER, OP_BACKWARD = range(7)
 W_GATE_UP, W_DOWN = 0, 1
-OP_GROUPED_LINEAR, OP_GROUPED_DX, OP_GROUPED_DW = range(3)
+OP_GROUPED_LINEAR, OP_GROUPED_DX, OP_GROUPED_DW, OP_GROUPED_FP4 = range(4)
+SCORES = {"softmax": 0, "sigmoid": 1}
+GROUP_SCORES = {"max": 0, "top2": 1}
 ACTIVATIONS = {"none": 0, "relu": 1, "relu2": 2, "silu": 3, "gelu_tanh": 4}
 
 EXPORTS = ("moe_status_str", "moe_problem_check", "moe_workspace_bytes", "moe_packed_bytes",
@@ -44,7 +48,9 @@ EXPORTS = ("moe_status_str", "moe_problem_check", "moe_workspace_bytes", "moe_pa
            "moe_layer_backward", "moe_debug_status", "moe_layer_static",
            "moe_layer_static_max_bytes", "moe_grouped_check", "moe_grouped_workspace_bytes",
            "moe_grouped_linear", "moe_grouped_linear_dx", "moe_grouped_linear_dw",
-           "moe_activation_backward")
+           "moe_activation_backward", "moe_route_scored", "moe_router_scored",
+           "moe_route_scored_backward", "moe_quantize_fp4", "moe_dequantize_fp4",
+           "moe_quantize_fp4_weights", "moe_grouped_linear_fp4")
 
 
 class MoeError(RuntimeError):
@@ -77,6 +83,15 @@ class MoeGrouped(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("R", "T", "K", "N", "E")]
 
 
+class MoeScoring(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("score", "n_group", "topk_group", "group_score")]
+    _fields_ += [("scale", ctypes.c_double)]
+
+
+class MoeFp4Weights(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("codes", "scales", "bias")]
+
+
 def _load(path: str = LIB_PATH) -> ctypes.CDLL:
     if not os.path.exists(path):
         raise ImportError(f"{path} is not built; run `python expert_ffn_moe_amd/build.py` "
@@ -85,6 +100,7 @@ def _load(path: str = LIB_PATH) -> ctypes.CDLL:
     P = ctypes.c_void_p
     PP = ctypes.POINTER(MoeProblem)
     PG = ctypes.POINTER(MoeGrouped)
+    PS, PW = ctypes.POINTER(MoeScoring), ctypes.POINTER(MoeFp4Weights)
     i32, i64 = ctypes.c_int32, ctypes.c_int64
     sz = ctypes.c_size_t
     sigs = {
@@ -124,6 +140,14 @@ def _load(path: str = LIB_PATH) -> ctypes.CDLL:
         "moe_grouped_linear_dx": (ctypes.c_int, [PG, P, P, P, ctypes.c_int, P, P, P, P, P, sz, P]),
         "moe_grouped_linear_dw": (ctypes.c_int, [PG, P, P, P, P, ctypes.c_int, P, P, P, sz, P]),
         "moe_activation_backward": (ctypes.c_int, [i64, i32, P, ctypes.c_int, P, P, P, P, P, P]),
+        "moe_route_scored": (ctypes.c_int, [PP, PS, P, P, P, P, P, P, sz, P]),
+        "moe_router_scored": (ctypes.c_int, [PP, PS, P, P, P, P, P, P, P, P, sz, P]),
+        "moe_route_scored_backward": (ctypes.c_int, [PP, PS, P, P, P, P, P, P]),
+        "moe_quantize_fp4": (ctypes.c_int, [P, i64, i32, P, P, P, P]),
+        "moe_dequantize_fp4": (ctypes.c_int, [P, P, i64, i32, P, P, P]),
+        "moe_quantize_fp4_weights": (ctypes.c_int, [P, i32, i32, i32, P, P, P]),
+        "moe_grouped_linear_fp4": (ctypes.c_int, [PG, ctypes.c_int, P, P, P, P, PW, PW,
+                                                  ctypes.c_int, P, P, P, sz, P]),
     }
     for name, (res, args) in sigs.items():
         fn = getattr(lib, name)
@@ -770,3 +794,202 @@ def activation_backward(dy, checkpoint, act: str, live_rows=None, out=None, a=No
             _arg(scales, "scales", (rows, cols // QBLOCK), torch.uint8, dev),
             _arg(dz, "out", shape, bf, dev), _arg(a, "a", shape, bf, dev))
     return dz
+
+
+# ---- routing by scores (see moe_route_scored and the calls with it in include/moe.h)
+@dataclasses.dataclass(frozen=True)
+class Scoring:
+    """How experts are scored and chosen (moe_scoring): score "softmax" or "sigmoid", a limit to
+    the best topk_group of n_group groups by group_score "max" or "top2" (the sum of the two
+    best), and the factor on the weights."""
+    score: str = "softmax"
+    n_group: int = 1
+    topk_group: int = 1
+    group_score: str = "max"
+    scale: float = 1.0
+
+    def __post_init__(self):
+        if self.score not in SCORES:
+            raise ValueError(f"unknown score {self.score!r}; one of {', '.join(SCORES)}")
+        if self.group_score not in GROUP_SCORES:
+            raise ValueError(f"unknown group score {self.group_score!r}; one of "
+                             f"{', '.join(GROUP_SCORES)}")
+        c = MoeScoring(SCORES[self.score], self.n_group, self.topk_group,
+                       GROUP_SCORES[self.group_score], self.scale)
+        object.__setattr__(self, "_c", c)
+        object.__setattr__(self, "_ref", ctypes.byref(c))
+
+    def __reduce__(self):  # as GroupedProblem
+        return type(self), (self.score, self.n_group, self.topk_group, self.group_score,
+                            self.scale)
+
+
+@functools.lru_cache(maxsize=256)
+def _problem_ref(p: Problem):
+    """(the C struct, a reference to it, the routing workspace's bytes) of a problem"""
+    c = p.c()
+    return c, ctypes.byref(c), p.workspace_bytes(OP_ROUTE)
+
+
+def _routing_out(p: Problem, out, device, index: int):
+    """(outputs, their addresses) of a routing call on GPU `index`"""
+    shape = (p.T, p.k)
+    if out is None:
+        out = (_empty(shape, torch.int32, device), _empty(shape, torch.float32, device),
+               _empty(shape, torch.uint8, device))
+    ids, w, keep = out
+    return out, (_arg(ids, "topk_ids", shape, torch.int32, index),
+                 _arg(w, "topk_w", shape, torch.float32, index),
+                 _arg(keep, "keep", shape, torch.uint8, index))
+
+
+def _ws_arg(ws, need: int, device):
+    """(workspace or None, its address, its bytes)"""
+    if ws is None:
+        if need == 0:
+            return None, None, 0
+        ws = torch.empty(need, dtype=torch.uint8, device=device)
+    elif ws.dtype != torch.uint8 or ws.device != device or not ws.is_contiguous():
+        raise ValueError(f"ws must be a contiguous uint8 tensor on {device}")
+    return ws, ws.data_ptr(), ws.numel()
+
+
+def route_scored(p: Problem, logits, scoring: Scoring, bias=None, out=None, ws=None):
+    """Top-k by scores (+ bias [E] f32) under scoring's group limit, and the capacity: returns
+    (topk_ids [T, k] i32, topk_w [T, k] f32, keep [T, k] u8).  A logit of -inf or NaN takes its
+    expert out."""
+    f32, shape = torch.float32, (p.T, p.E)
+    dev = _first(logits, "logits", shape, f32)
+    _, ref, need = _problem_ref(p)
+    out, ptrs = _routing_out(p, out, logits.device, dev)
+    ws, wsp, wsn = _ws_arg(ws, need, logits.device)
+    _launch("moe_route_scored", dev, ref, scoring._ref, _arg(logits, "logits", shape, f32, dev),
+            _arg(bias, "bias", (p.E,), f32, dev), *ptrs, wsp, wsn)
+    return out
+
+
+def router_scored(p: Problem, x, w_router, scoring: Scoring, bias=None, logits=None,
+                  want_logits: bool = False, out=None, ws=None):
+    """Router GEMM (logits = x w_router^T, w_router [E, H]) and route_scored in one call.  Returns
+    (topk_ids, topk_w, keep, logits) -- logits None unless asked for (or passed in)."""
+    f32, bf = torch.float32, torch.bfloat16
+    dev = _first(x, "x", (p.T, p.H), bf)
+    _, ref, _ = _problem_ref(p)
+    if logits is None and want_logits:
+        logits = _empty((p.T, p.E), f32, x.device)
+    out, ptrs = _routing_out(p, out, x.device, dev)
+    ws, wsp, wsn = _ws_arg(ws, p.workspace_bytes(OP_ROUTER) if ws is None else 0, x.device)
+    _launch("moe_router_scored", dev, ref, scoring._ref, _arg(x, "x", (p.T, p.H), bf, dev),
+            _arg(w_router, "w_router", (p.E, p.H), bf, dev), _arg(bias, "bias", (p.E,), f32, dev),
+            _arg(logits, "logits", (p.T, p.E), f32, dev), *ptrs, wsp, wsn)
+    return (*out, logits)
+
+
+def route_scored_backward(p: Problem, logits, scoring: Scoring, topk_ids, topk_w, dtopk_w,
+                          out=None):
+    """dlogits [T, E] f32 of route_scored from dtopk_w [T, k] f32 (0 for dropped slots), with the
+    forward's logits, topk_ids and topk_w."""
+    f32, shape, slots = torch.float32, (p.T, p.E), (p.T, p.k)
+    dev = _first(logits, "logits", shape, f32)
+    _, ref, _ = _problem_ref(p)
+    dlogits = _empty(shape, f32, logits.device) if out is None else out
+    _launch("moe_route_scored_backward", dev, ref, scoring._ref,
+            _arg(logits, "logits", shape, f32, dev),
+            _arg(topk_ids, "topk_ids", slots, torch.int32, dev),
+            _arg(topk_w, "topk_w", slots, f32, dev), _arg(dtopk_w, "dtopk_w", slots, f32, dev),
+            _arg(dlogits, "out", shape, f32, dev))
+    return dlogits
+
+
+# ---- microscaled 4-bit values (see moe_quantize_fp4 and the calls after it in include/moe.h)
+def _fp4_shapes(shape):
+    if len(shape) < 2:
+        raise ValueError("rows of 32-value blocks are needed: at least 2-D")
+    if shape[-1] % QBLOCK or shape[-1] == 0:
+        raise ValueError(f"the last dimension must be a positive multiple of {QBLOCK}, not "
+                         f"{shape[-1]}")
+    lead = tuple(shape[:-1])
+    return lead + (shape[-1] // 2,), lead + (shape[-1] // QBLOCK,)
+
+
+def quantize_fp4(x, live_rows=None, out=None):
+    """4-bit form of bf16 x [..., C] (C a multiple of 32): (codes [..., C/2] u8, value 2 i in the
+    low half of byte i, scales [..., C/32] u8).  live_rows: an i32 tensor of one element; rows
+    from there on are neither read nor written."""
+    u8, bf = torch.uint8, torch.bfloat16
+    cs, ss = _fp4_shapes(x.shape)
+    dev = _first(x, "x", x.shape, bf)
+    codes, scales = out if out is not None else (_empty(cs, u8, x.device),
+                                                 _empty(ss, u8, x.device))
+    cols = x.shape[-1]
+    _launch("moe_quantize_fp4", dev, _arg(x, "x", x.shape, bf, dev), x.numel() // cols, cols,
+            _arg(live_rows, "live_rows", (1,), torch.int32, dev),
+            _arg(codes, "codes", cs, u8, dev), _arg(scales, "scales", ss, u8, dev))
+    return codes, scales
+
+
+def dequantize_fp4(codes, scales, live_rows=None, out=None):
+    """The bf16 values [..., C] of a 4-bit form (exact); live_rows as quantize_fp4."""
+    u8, bf = torch.uint8, torch.bfloat16
+    shape = tuple(codes.shape[:-1]) + (2 * codes.shape[-1],)
+    cs, ss = _fp4_shapes(shape)
+    dev = _first(codes, "codes", cs, u8)
+    values = _empty(shape, bf, codes.device) if out is None else out
+    cols = shape[-1]
+    _launch("moe_dequantize_fp4", dev, _arg(codes, "codes", cs, u8, dev),
+            _arg(scales, "scales", ss, u8, dev), values.numel() // cols, cols,
+            _arg(live_rows, "live_rows", (1,), torch.int32, dev),
+            _arg(values, "out", shape, bf, dev))
+    return values
+
+
+def quantize_fp4_weights(w, out=None):
+    """4-bit form of bf16 weights [E, K, N], blocks along K: (codes [E, N, K/2] u8, scales
+    [E, N, K/32] u8), as grouped_linear_fp4 takes them."""
+    if w.dim() != 3:
+        raise ValueError("w must be [E, K, N]")
+    u8, bf = torch.uint8, torch.bfloat16
+    E, K, N = w.shape
+    cs, ss = (E, N, K // 2), (E, N, K // QBLOCK)
+    dev = _first(w, "w", w.shape, bf)
+    codes, scales = out if out is not None else (_empty(cs, u8, w.device),
+                                                 _empty(ss, u8, w.device))
+    _launch("moe_quantize_fp4_weights", dev, _arg(w, "w", w.shape, bf, dev), E, K, N,
+            _arg(codes, "codes", cs, u8, dev), _arg(scales, "scales", ss, u8, dev))
+    return codes, scales
+
+
+def _fp4_weights(p: GroupedProblem, w, bias, what: str, index: int) -> MoeFp4Weights:
+    codes, scales = w
+    u8 = torch.uint8
+    return MoeFp4Weights(_arg(codes, f"{what} codes", (p.E, p.N, p.K // 2), u8, index),
+                         _arg(scales, f"{what} scales", (p.E, p.N, p.K // QBLOCK), u8, index),
+                         _arg(bias, f"{what} bias", (p.E, p.N), torch.bfloat16, index))
+
+
+def grouped_linear_fp4(p: GroupedProblem, x, w, offsets=None, up=None, bias=None, up_bias=None,
+                       act: str = "none", residual=None, row_token=None, out=None, ws=None):
+    """y[r] = act(x[r] w[e] + bias[e]) * (x[r] up[e] + up_bias[e]) + residual[r] for the rows of
+    each expert; without up its factor is left out.  w, up: (codes, scales) of
+    quantize_fp4_weights; x: (codes, scales) of quantize_fp4 (codes [R, K/2]) or quantize_fp8
+    ([R, K]), [T, .] read through row_token.  Returns y [R, N]; rows behind the last expert's are
+    left as they were."""
+    bf, u8, R, K, N = torch.bfloat16, torch.uint8, p.R, p.K, p.N
+    codes, scales = x
+    rows = R if row_token is None else p.x_tokens
+    eight = isinstance(codes, torch.Tensor) and codes.dim() == 2 and codes.shape[1] == K
+    xs = (rows, K if eight else K // 2)
+    dev = _first(codes, "x codes", xs, u8)
+    if up is None and up_bias is not None:
+        raise ValueError("up_bias needs up")
+    y = _empty((R, N), bf, codes.device) if out is None else out
+    wc = _fp4_weights(p, w, bias, "w", dev)
+    uc = ctypes.byref(_fp4_weights(p, up, up_bias, "up", dev)) if up is not None else None
+    ws, wsp, wsn = _grouped_ws(p, OP_GROUPED_FP4, ws, codes)
+    _launch("moe_grouped_linear_fp4", dev, p._ref, MOE_FP8 if eight else MOE_FP4,
+            _arg(codes, "x codes", xs, u8, dev),
+            _arg(scales, "x scales", (rows, K // QBLOCK), u8, dev),
+            _arg(row_token, "row_token", (R,), torch.int32, dev), _offsets_arg(p, offsets, dev),
+            ctypes.byref(wc), uc, _act(act), _arg(residual, "residual", (R, N), bf, dev),
+            _arg(y, "out", (R, N), bf, dev), wsp, wsn)
+    return y

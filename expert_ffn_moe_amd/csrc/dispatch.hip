@@ -392,7 +392,9 @@ hipError_t launch_layout(const moe_problem& p, const int32_t* ids, const uint8_t
   hipLaunchKernelGGL((scatter_kernel<HK, CAND>), grid, dim3(64 * kLayoutWaves), lds, s, ids,   \
                      keep, p.T, p.E, p.k, nchunks, chunk_base, counts, offsets, row_token,     \
                      slot_to_row, cand_slot)
-  if (cand_slot)
+  if (cand_slot && keep)
+    MOE_SCATTER(true, true);
+  else if (cand_slot)
     MOE_SCATTER(false, true);
   else if (keep)
     MOE_SCATTER(true, false);

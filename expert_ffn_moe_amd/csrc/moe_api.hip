@@ -4,11 +4,14 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 #include <initializer_list>
 #include <mutex>
 
+#include "fp4_launch.h"
 #include "grouped_launch.h"
 #include "moe_internal.h"
+#include "scored.h"
 
 namespace moe {
 
@@ -303,11 +306,12 @@ size_t natural_w_bytes(const moe_problem& p) {  // one natural weight set [E, H,
 }
 
 // Capacity after the selection: candidate layout + radix select (no-op without a cap).
+// candidates: NULL (every slot), or keep flags of the slots that count.
 hipError_t run_capacity(const moe_problem& p, int32_t* ids, float* w, uint8_t* keep,
-                        const RankScratch& r, hipStream_t s) {
+                        const RankScratch& r, hipStream_t s, const uint8_t* candidates = nullptr) {
   hipError_t err = hipSuccess;
   if (p.capacity <= 0) return err;
-  if ((err = launch_layout(p, ids, nullptr, r.chunk_hist, r.chunk_base, r.cand_counts,
+  if ((err = launch_layout(p, ids, candidates, r.chunk_hist, r.chunk_base, r.cand_counts,
                            r.cand_offsets, nullptr, nullptr, r.cand_slot, s)) != hipSuccess)
     return err;
   return launch_capacity_select(p, r.cand_counts, r.cand_offsets, r.cand_slot, w, keep, s);
@@ -325,6 +329,12 @@ hipError_t run_route(const moe_problem& p, const float* logits, int n_group, int
 bool groups_ok(const moe_problem& p, int n_group, int topk_group) {
   return n_group >= 1 && n_group <= 64 && p.E % n_group == 0 && topk_group >= 1 &&
          topk_group <= n_group && (int64_t)topk_group * (p.E / n_group) >= p.k;
+}
+
+bool scoring_ok(const moe_problem& p, const moe_scoring& sc) {
+  return (sc.score == MOE_SCORE_SOFTMAX || sc.score == MOE_SCORE_SIGMOID) &&
+         (sc.group_score == MOE_GROUP_MAX || sc.group_score == MOE_GROUP_TOP2) && (float)sc.scale > 0.0f &&
+         std::isfinite((float)sc.scale) && groups_ok(p, sc.n_group, sc.topk_group);
 }
 
 hipError_t run_dispatch(const moe_problem& p, const void* x, const int32_t* ids,
@@ -404,6 +414,13 @@ void* static_scratch() {
   return g_scratch_ptr[dev];
 }
 
+// ---- microscaled 4-bit values
+constexpr int kFp4Block = 32;  // values per scale
+// rows x cols values in blocks along the columns, as the calls' contract has them.
+bool fp4_rows_ok(int64_t rows, int32_t cols) {
+  return rows >= 0 && cols >= 1 && cols % kFp4Block == 0 && rows <= ((int64_t)1 << 39) / cols;
+}
+
 // ---- grouped linear products
 constexpr int kCkptBlock = 32;  // columns per scale of an 8-bit checkpoint
 bool act_ok(int act) { return act >= MOE_ACT_NONE && act <= MOE_ACT_GELU_TANH; }
@@ -423,8 +440,12 @@ bool grouped_args_ok(const moe_grouped& g, const int32_t* offsets,
     if (!aligned16(q)) return false;
   return true;
 }
+size_t grouped_op_ws_bytes(const moe_grouped& g, int op) {
+  if (op != MOE_GROUPED_FP4) return grouped_ws_bytes(g, op);
+  return g.K % kFp4Block ? 0 : grouped_fp4_ws_bytes(g);
+}
 int check_grouped_ws(const moe_grouped& g, int op, const void* ws, size_t ws_bytes) {
-  const size_t need = grouped_ws_bytes(g, op);
+  const size_t need = grouped_op_ws_bytes(g, op);
   if (need == 0) return MOE_OK;
   if (!ws) return MOE_ERR_WORKSPACE;
   if (((uintptr_t)ws & 255) != 0) return MOE_ERR_INVALID_ARG;
@@ -577,6 +598,110 @@ int moe_router(const moe_problem* p, const void* x, const void* w_router, int32_
                                  topk_w, keep, s);
   if (err == hipSuccess) err = run_capacity(*p, topk_ids, topk_w, keep, r.rank, s);
   return status_of(err);
+}
+
+int moe_route_scored(const moe_problem* p, const moe_scoring* sc, const float* logits,
+                     const float* bias, int32_t* topk_ids, float* topk_w, uint8_t* keep, void* ws,
+                     size_t ws_bytes, void* stream) {
+  int st = moe_problem_check(p);
+  if (st != MOE_OK) return st;
+  if (!sc || !logits || !topk_ids || !topk_w || !keep || !scoring_ok(*p, *sc))
+    return MOE_ERR_INVALID_ARG;
+  if (aliased({{topk_ids, tk_of(*p) * 4}, {topk_w, tk_of(*p) * 4}, {keep, tk_of(*p)},
+               {ws, ws_bytes}},
+              {{logits, (size_t)p->T * p->E * 4}, {bias, (size_t)p->E * 4}}))
+    return MOE_ERR_INVALID_ARG;
+  if ((st = check_ws(p, MOE_OP_ROUTE, ws, ws_bytes)) != MOE_OK) return st;
+  Carve c(ws);
+  RankScratch r = carve_route(c, *p);
+  if (c.used > ws_bytes) return MOE_ERR_WORKSPACE;  // (sized by the same carve)
+  hipStream_t s = as_stream(stream);
+  hipError_t err = launch_route_scored(*p, *sc, logits, 1, bias, nullptr, topk_ids, topk_w, keep, s);
+  if (err == hipSuccess) err = run_capacity(*p, topk_ids, topk_w, keep, r, s, keep);
+  return status_of(err);
+}
+
+int moe_router_scored(const moe_problem* p, const moe_scoring* sc, const void* x,
+                      const void* w_router, const float* bias, float* logits, int32_t* topk_ids,
+                      float* topk_w, uint8_t* keep, void* ws, size_t ws_bytes, void* stream) {
+  int st = moe_problem_check(p);
+  if (st != MOE_OK) return st;
+  if (!sc || !x || !w_router || !topk_ids || !topk_w || !keep || !scoring_ok(*p, *sc))
+    return MOE_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(w_router)) return MOE_ERR_INVALID_ARG;
+  if (!router_supported(*p)) return MOE_ERR_UNSUPPORTED;
+  if (aliased({{logits, (size_t)p->T * p->E * 4}, {topk_ids, tk_of(*p) * 4},
+               {topk_w, tk_of(*p) * 4}, {keep, tk_of(*p)}, {ws, ws_bytes}},
+              {{x, (size_t)p->T * p->H * 2}, {w_router, (size_t)p->E * p->H * 2},
+               {bias, (size_t)p->E * 4}}))
+    return MOE_ERR_INVALID_ARG;
+  if ((st = check_ws(p, MOE_OP_ROUTER, ws, ws_bytes)) != MOE_OK) return st;
+  Carve c(ws);
+  RouterScratch r = carve_router(c, *p);
+  if (c.used > ws_bytes) return MOE_ERR_WORKSPACE;
+  hipStream_t s = as_stream(stream);
+  hipError_t err = launch_router_logits(*p, x, w_router, r.part, s);
+  if (err == hipSuccess)
+    err = launch_route_scored(*p, *sc, r.part, router_plan(*p).split, bias, logits, topk_ids,
+                              topk_w, keep, s);
+  if (err == hipSuccess) err = run_capacity(*p, topk_ids, topk_w, keep, r.rank, s, keep);
+  return status_of(err);
+}
+
+int moe_route_scored_backward(const moe_problem* p, const moe_scoring* sc, const float* logits,
+                              const int32_t* topk_ids, const float* topk_w, const float* dtopk_w,
+                              float* dlogits, void* stream) {
+  const int st = moe_problem_check(p);
+  if (st != MOE_OK) return st;
+  if (!sc || !logits || !topk_ids || !topk_w || !dtopk_w || !dlogits || !scoring_ok(*p, *sc))
+    return MOE_ERR_INVALID_ARG;
+  const size_t te = (size_t)p->T * p->E * 4, tk = tk_of(*p) * 4;
+  if (aliased({{dlogits, te}}, {{logits, te}, {topk_ids, tk}, {topk_w, tk}, {dtopk_w, tk}}))
+    return MOE_ERR_INVALID_ARG;
+  hipStream_t s = as_stream(stream);
+  hipError_t err = hipSuccess;
+#ifdef MOE_DEBUG_CHECKS
+  err = launch_check_ids(*p, topk_ids, s);
+#endif
+  if (err == hipSuccess)
+    err = launch_route_scored_bwd(*p, *sc, logits, topk_ids, topk_w, dtopk_w, dlogits, s);
+  return status_of(err);
+}
+
+int moe_quantize_fp4(const void* x, int64_t rows, int32_t cols, const int32_t* live_rows,
+                     uint8_t* codes, uint8_t* scales, void* stream) {
+  if (!fp4_rows_ok(rows, cols)) return MOE_ERR_INVALID_ARG;
+  if (rows == 0) return MOE_OK;
+  if (!x || !codes || !scales || !aligned16(x) || !aligned16(codes)) return MOE_ERR_INVALID_ARG;
+  const size_t n = (size_t)rows * cols;
+  if (aliased({{codes, n / 2}, {scales, n / kFp4Block}}, {{x, 2 * n}, {live_rows, 4}}))
+    return MOE_ERR_INVALID_ARG;
+  return status_of(
+      launch_quantize_fp4(x, rows, cols, live_rows, codes, scales, as_stream(stream)));
+}
+
+int moe_dequantize_fp4(const uint8_t* codes, const uint8_t* scales, int64_t rows, int32_t cols,
+                       const int32_t* live_rows, void* out, void* stream) {
+  if (!fp4_rows_ok(rows, cols)) return MOE_ERR_INVALID_ARG;
+  if (rows == 0) return MOE_OK;
+  if (!codes || !scales || !out || !aligned16(codes) || !aligned16(out))
+    return MOE_ERR_INVALID_ARG;
+  const size_t n = (size_t)rows * cols;
+  if (aliased({{out, 2 * n}}, {{codes, n / 2}, {scales, n / kFp4Block}, {live_rows, 4}}))
+    return MOE_ERR_INVALID_ARG;
+  return status_of(
+      launch_dequantize_fp4(codes, scales, rows, cols, live_rows, out, as_stream(stream)));
+}
+
+int moe_quantize_fp4_weights(const void* w, int32_t E, int32_t K, int32_t N, uint8_t* codes,
+                             uint8_t* scales, void* stream) {
+  if (E < 1 || K < 1 || N < 1 || !w || !codes || !scales || !aligned16(w) || !aligned16(codes))
+    return MOE_ERR_INVALID_ARG;
+  if (E > kMaxE || K % kFp4Block || N % 8 || K > (1 << 20) || N > (1 << 20))
+    return MOE_ERR_UNSUPPORTED;
+  const size_t n = (size_t)E * K * N;
+  if (aliased({{codes, n / 2}, {scales, n / kFp4Block}}, {{w, 2 * n}})) return MOE_ERR_INVALID_ARG;
+  return status_of(launch_quantize_fp4_weights(w, E, K, N, codes, scales, as_stream(stream)));
 }
 
 int moe_dispatch(const moe_problem* p, const void* x, const int32_t* topk_ids,
@@ -950,8 +1075,8 @@ int moe_grouped_check(const moe_grouped* g) {
 }
 
 size_t moe_grouped_workspace_bytes(const moe_grouped* g, int op) {
-  if (moe_grouped_check(g) != MOE_OK || op < MOE_GROUPED_LINEAR || op > MOE_GROUPED_DW) return 0;
-  return grouped_ws_bytes(*g, op);
+  if (moe_grouped_check(g) != MOE_OK || op < MOE_GROUPED_LINEAR || op > MOE_GROUPED_FP4) return 0;
+  return grouped_op_ws_bytes(*g, op);
 }
 
 int moe_grouped_linear(const moe_grouped* g, const void* x, const int32_t* row_token,
@@ -1041,6 +1166,38 @@ int moe_activation_backward(int64_t rows, int32_t cols, const int32_t* live_rows
   if (rows == 0) return MOE_OK;
   return status_of(launch_act_backward(rows, cols, live_rows, act, dy, z_codes, z_scales, dz, a,
                                        as_stream(stream)));
+}
+
+int moe_grouped_linear_fp4(const moe_grouped* g, int x_dtype, const uint8_t* x_codes,
+                           const uint8_t* x_scales, const int32_t* row_token,
+                           const int32_t* offsets, const moe_fp4_weights* w,
+                           const moe_fp4_weights* up, int act, const void* residual, void* y,
+                           void* ws, size_t ws_bytes, void* stream) {
+  int st = moe_grouped_check(g);
+  if (st != MOE_OK) return st;
+  if (!w || !w->codes || !w->scales || (up && (!up->codes || !up->scales)) ||
+      (x_dtype != MOE_FP4 && x_dtype != MOE_FP8) || !act_ok(act) ||
+      !grouped_args_ok(*g, offsets, {x_codes, w->codes, w->bias, up ? up->codes : nullptr,
+                                     up ? up->bias : nullptr, residual, y}) ||
+      (g->R > 0 && (!x_codes || !x_scales || !y || (row_token && g->T < 1))))
+    return MOE_ERR_INVALID_ARG;
+  if (g->K % kFp4Block) return MOE_ERR_UNSUPPORTED;
+  const moe_fp4_weights none{}, &u = up ? *up : none;
+  const size_t xn = (size_t)(row_token ? g->T : g->R) * g->K, wn = grouped_w(*g);
+  const size_t yb = rows_bf16(g->R, g->N), bb = rows_bf16(g->E, g->N);
+  if (aliased({{y, yb}, {ws, ws_bytes}},
+              {{x_codes, x_dtype == MOE_FP4 ? xn / 2 : xn}, {x_scales, xn / kFp4Block},
+               {row_token, (size_t)g->R * 4}, {offsets, ((size_t)g->E + 1) * 4},
+               {w->codes, wn / 2}, {w->scales, wn / kFp4Block}, {w->bias, bb},
+               {u.codes, wn / 2}, {u.scales, wn / kFp4Block}, {u.bias, bb}, {residual, yb}}))
+    return MOE_ERR_INVALID_ARG;
+  if ((st = check_grouped_ws(*g, MOE_GROUPED_FP4, ws, ws_bytes)) != MOE_OK) return st;
+  if (g->R == 0) return MOE_OK;
+  hipError_t err = check_grouped_device(*g, offsets, row_token, as_stream(stream));
+  if (err == hipSuccess)
+    err = launch_grouped_fp4(*g, x_dtype == MOE_FP8, x_codes, x_scales, row_token, offsets, *w, u,
+                             act, residual, y, ws, as_stream(stream));
+  return status_of(err);
 }
 
 size_t moe_layer_chunked_workspace_bytes(const moe_problem* p, int32_t chunk_tokens,

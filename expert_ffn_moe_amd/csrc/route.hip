@@ -12,6 +12,7 @@
 //   slots (or of EXP(l_e - m) over all experts e = 0..E-1 without renormalisation);
 //   w_j = e_j / S with IEEE division.  No contraction anywhere in this file.
 #include "moe_internal.h"
+#include "scored.h"
 #include "wave.h"
 
 #pragma clang fp contract(off)
@@ -415,16 +416,13 @@ RouterPlan router_plan(const moe_problem& p) {
   return plan;
 }
 
-hipError_t launch_router(const moe_problem& p, const void* x, const void* wr, int n_group,
-                         int topk_group, float* part, float* logits, int32_t* ids, float* w,
-                         uint8_t* keep, hipStream_t s) {
+hipError_t launch_router_logits(const moe_problem& p, const void* x, const void* wr, float* part,
+                                hipStream_t s) {
   const RouterPlan plan = router_plan(p);
-  hipError_t err;
   switch (p.E / 16) {
 #define MOE_ROUTER_CASE(n) \
   case n:                  \
-    err = launch_router_gemm_t<n>(p, plan, x, wr, part, s); \
-    break;
+    return launch_router_gemm_t<n>(p, plan, x, wr, part, s);
     MOE_ROUTER_CASE(1) MOE_ROUTER_CASE(2) MOE_ROUTER_CASE(3) MOE_ROUTER_CASE(4)
     MOE_ROUTER_CASE(5) MOE_ROUTER_CASE(6) MOE_ROUTER_CASE(7) MOE_ROUTER_CASE(8)
     MOE_ROUTER_CASE(9) MOE_ROUTER_CASE(10) MOE_ROUTER_CASE(11) MOE_ROUTER_CASE(12)
@@ -433,8 +431,14 @@ hipError_t launch_router(const moe_problem& p, const void* x, const void* wr, in
     default:
       return hipErrorInvalidValue;
   }
+}
+
+hipError_t launch_router(const moe_problem& p, const void* x, const void* wr, int n_group,
+                         int topk_group, float* part, float* logits, int32_t* ids, float* w,
+                         uint8_t* keep, hipStream_t s) {
+  const hipError_t err = launch_router_logits(p, x, wr, part, s);
   if (err != hipSuccess) return err;
-  return launch_select(p, part, plan.split, n_group, topk_group, logits, ids, w, keep, s);
+  return launch_select(p, part, router_plan(p).split, n_group, topk_group, logits, ids, w, keep, s);
 }
 
 }  // namespace moe

@@ -14,6 +14,10 @@
  *   moe_grouped_linear  one product per expert over its rows, with bias, activation and
  *                    residual, and its gradients (moe_grouped_linear_dx, _dw,
  *                    moe_activation_backward) from pre-activations kept in 8 bits
+ *   moe_route_scored  routing by softmax or sigmoid scores with a bias for balance, from the
+ *                    logits or the hidden states (moe_router_scored), and its gradient
+ *   moe_quantize_fp4  4-bit values with block scales (weights: moe_quantize_fp4_weights) and back
+ *   moe_grouped_linear_fp4  moe_grouped_linear on 4-bit weights, optionally gated
  *
  * The pages describe the operations in prose; each declaration names the passage:
  *   [axolotl]  docs.axolotl.ai "integrations.expert_parallel.args", attribute table
@@ -79,8 +83,9 @@ typedef enum {
  * (largest finite 448, round to nearest even, saturating) with one UE8M0 scale byte
  * (value 2^(byte-127)) per 32 consecutive elements along the reduction dimension; the
  * scale of a block is the smallest power of two 2^e with max|x| <= 448 * 2^e (2^0 for an
- * all-zero block). */
-typedef enum { MOE_F32 = 0, MOE_BF16 = 1, MOE_FP8 = 2 } moe_dtype;
+ * all-zero block).
+ * MOE_FP4 (only moe_grouped_linear_fp4's x): see moe_quantize_fp4; no moe_problem takes it. */
+typedef enum { MOE_F32 = 0, MOE_BF16 = 1, MOE_FP8 = 2, MOE_FP4 = 3 } moe_dtype;
 
 /* Problem description.  T tokens of width H, E experts, top-k, SwiGLU width I. */
 typedef struct {
@@ -480,7 +485,8 @@ typedef enum {
 typedef enum {
   MOE_GROUPED_LINEAR = 0,
   MOE_GROUPED_DX = 1,
-  MOE_GROUPED_DW = 2
+  MOE_GROUPED_DW = 2,
+  MOE_GROUPED_FP4 = 3 /* moe_grouped_linear_fp4, with or without a second weight set */
 } moe_grouped_op;
 
 /* MOE_OK, MOE_ERR_INVALID_ARG (g NULL, R or T < 0, K, N or E < 1) or MOE_ERR_UNSUPPORTED
@@ -551,6 +557,115 @@ int moe_grouped_linear_dw(const moe_grouped* g, const void* x, const int32_t* ro
 int moe_activation_backward(int64_t rows, int32_t cols, const int32_t* live_rows, int act,
                             const void* dy, const uint8_t* z_codes, const uint8_t* z_scales,
                             void* dz, void* a, void* stream);
+
+/* ---------------------------------------------------------------------------------
+ * Routing by scores -- [LightLLM] call-order paragraph: `experts()` does grouped top-k inside the
+ * layer; the pages give neither the score nor the group rule, and moe_route_grouped reads them
+ * as logits and their maximum.  Here they are arguments:
+ *   score        s[t, e]: the softmax of the token's logits, or the sigmoid of each
+ *   bias [E] f32 or NULL: added to the scores for the choice alone (a bias that a training loop
+ *                moves to balance the experts' loads); the weights come from the scores
+ *   n_group, topk_group  as moe_route_grouped
+ *   group_score  MOE_GROUP_MAX: a group's largest s + bias; MOE_GROUP_TOP2: the sum of its two
+ *                largest (of the one where it has no more)
+ *   p->renormalize  1: w = scale * s / (sum of the k chosen scores), zeros where that sum is zero;
+ *                0: w = scale * s
+ *   scale        > 0 and finite in 32 bits
+ * Without a bias experts are ordered by their logits, with which the scores rise.  Ties go to the
+ * lower expert (group) id.  Scores, choices and weights are computed in 64 bits, each weight
+ * rounded once to f32.
+ *
+ * An expert is out for a token where its logit is NaN or -inf, or its bias is (+inf counts as the
+ * largest f32).  It takes no part in the group scores and the choice, with such a logit nor in
+ * the softmax (the bias, which concerns the choice alone, leaves it there); where fewer than
+ * k experts of the taken groups are in, the last slots hold those that are out, lowest id first
+ * (so that a token's ids stay distinct), with weight 0 and keep 0.
+ *
+ * moe_route_scored: logits, topk_ids, topk_w, keep, capacity and workspace (MOE_OP_ROUTE) as
+ *   moe_route, slots in the order of the choice.  The capacity does not count slots whose expert is
+ *   out.  p->H and p->I are not used.
+ * moe_router_scored: from the hidden states: x, w_router, logits and workspace (MOE_OP_ROUTER) as
+ *   moe_router, whose restrictions on p apply.
+ * moe_route_scored_backward: the gradient of the logits from that of the weights,
+ *   dtopk_w [T, k] f32 (0 for slots the capacity dropped; slots whose topk_w is 0 are not read),
+ *   with the forward's logits, topk_ids and topk_w; dlogits [T, E] f32, written whole.  The choice
+ *   carries no gradient, nor does the bias; +inf logits get none.  sc's group fields are not used.
+ *   Needs no workspace.
+ * MOE_ERR_INVALID_ARG: unknown score or group_score, a scale that is not positive and finite, the
+ * group arguments as in moe_route_grouped.
+ * --------------------------------------------------------------------------------- */
+typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
+typedef enum { MOE_GROUP_MAX = 0, MOE_GROUP_TOP2 = 1 } moe_group_score;
+typedef struct {
+  int32_t score;       /* moe_score */
+  int32_t n_group;
+  int32_t topk_group;
+  int32_t group_score; /* moe_group_score */
+  double scale;
+} moe_scoring;
+
+int moe_route_scored(const moe_problem* p, const moe_scoring* sc, const float* logits,
+                     const float* bias, int32_t* topk_ids, float* topk_w, uint8_t* keep, void* ws,
+                     size_t ws_bytes, void* stream);
+int moe_router_scored(const moe_problem* p, const moe_scoring* sc, const void* x,
+                      const void* w_router, const float* bias, float* logits, int32_t* topk_ids,
+                      float* topk_w, uint8_t* keep, void* ws, size_t ws_bytes, void* stream);
+int moe_route_scored_backward(const moe_problem* p, const moe_scoring* sc, const float* logits,
+                              const int32_t* topk_ids, const float* topk_w, const float* dtopk_w,
+                              float* dlogits, void* stream);
+
+/* ---------------------------------------------------------------------------------
+ * Microscaled 4-bit values (OCP MXFP4; the block scales of MOE_FP8 with E2M1 codes): each block of
+ * 32 consecutive values of a row has one UE8M0 scale byte and 32 codes of +-{0, 0.5, 1, 1.5, 2, 3,
+ * 4, 6}, value 2 i in the low half of byte i.  The scale is the smallest power of two 2^e, e >=
+ * -127, with max|x| <= 6 * 2^e (2^0 for an all-zero block); values are rounded to nearest, ties to
+ * even.  A block with a value that is not finite gets the NaN scale byte 255 and zero codes: E2M1
+ * has no code for it, so all 32 read back as NaN.
+ *
+ * moe_quantize_fp4: x [rows, cols] bf16 -> codes [rows, cols/2] u8, scales [rows, cols/32] u8.
+ * moe_dequantize_fp4: back to out [rows, cols] bf16, exact (values of 2^128 and more: inf).
+ *   live_rows: device pointer, or NULL: rows from *live_rows on are neither read nor written.
+ *   rows = 0 enqueues nothing.  MOE_ERR_INVALID_ARG: rows < 0, cols not a positive multiple of 32,
+ *   rows * cols > 2^39, NULL or misaligned pointers (x, codes, out: 16 bytes).
+ * moe_quantize_fp4_weights: w [E, K, N] bf16 (the natural layout) -> codes [E, N, K/2], scales
+ *   [E, N, K/32], blocks along the reduction K: what moe_grouped_linear_fp4 reads, and what
+ *   moe_quantize_fp4 gives for the transposed weights.  MOE_ERR_INVALID_ARG: E, K or N < 1,
+ *   pointers as above; MOE_ERR_UNSUPPORTED: E > 1024, K % 32, N % 8, K or N above 2^20.
+ * --------------------------------------------------------------------------------- */
+int moe_quantize_fp4(const void* x, int64_t rows, int32_t cols, const int32_t* live_rows,
+                     uint8_t* codes, uint8_t* scales, void* stream);
+int moe_dequantize_fp4(const uint8_t* codes, const uint8_t* scales, int64_t rows, int32_t cols,
+                       const int32_t* live_rows, void* out, void* stream);
+int moe_quantize_fp4_weights(const void* w, int32_t E, int32_t K, int32_t N, uint8_t* codes,
+                             uint8_t* scales, void* stream);
+
+/* ---------------------------------------------------------------------------------
+ * moe_grouped_linear_fp4 -- moe_grouped_linear on weights of 4 bits, for serving: with r' =
+ * row_token ? row_token[r] : r and ^ for the values that codes and scales stand for,
+ *   y[r] = act(x^[r'] W^[e] + b[e]) * (x^[r'] U^[e] + c[e]) + residual[r]
+ * where the factor with U is left out without `up` (SwiGLU: act MOE_ACT_SILU, w the gate).
+ *   x_dtype   MOE_FP4: x_codes [R, K/2] from moe_quantize_fp4; MOE_FP8: x_codes [R, K] from
+ *             moe_quantize_fp8; x_scales [R, K/32]  ([T, .] with row_token [R] i32)
+ *   w, up     codes [E, N, K/2], scales [E, N, K/32] (moe_quantize_fp4_weights), bias [E, N] bf16
+ *             or NULL; up NULL: one weight set
+ *   residual  [R, N] bf16 or NULL;  y [R, N] bf16
+ * fp32 accumulation; y is rounded once.  With MOE_FP8 the matrix cores drop what lies more than
+ * 13 bits below a block's largest product.  A NaN scale or code makes its sums NaN.  Rows, offsets
+ * and row_token as in moe_grouped_linear, also where they are out of range.  Codes, residual, y and
+ * biases are 16-byte aligned, scales need no alignment.  MOE_ERR_UNSUPPORTED as moe_grouped_check,
+ * and unless K % 32 == 0.  Workspace: moe_grouped_workspace_bytes(g, MOE_GROUPED_FP4).
+ * --------------------------------------------------------------------------------- */
+typedef struct {
+  const uint8_t* codes;
+  const uint8_t* scales;
+  const void* bias;
+} moe_fp4_weights;
+
+int moe_grouped_linear_fp4(const moe_grouped* g, int x_dtype, const uint8_t* x_codes,
+                           const uint8_t* x_scales, const int32_t* row_token,
+                           const int32_t* offsets, const moe_fp4_weights* w,
+                           const moe_fp4_weights* up, int act, const void* residual, void* y,
+                           void* ws, size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

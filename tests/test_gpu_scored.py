@@ -1,0 +1,161 @@
+"""Routing by scores on the GPU against the fp64 definition: ids and keep flags equal, weights
+rounded once, the gradient within its roundings."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import scored
+from scored_common import INF, bias as make_bias, logits as make_logits, numpy_of
+
+pytestmark = pytest.mark.gpu
+
+
+def moe():
+    import expert_ffn_moe_amd
+
+    return expert_ffn_moe_amd
+
+
+# T, E, k, score, groups, taken, group score, bias, renorm, scale, capacity, logits
+CASES = [
+    (1, 256, 8, "sigmoid", 8, 4, "top2", "normal", True, 2.5, 0, "normal"),
+    (1, 1, 1, "sigmoid", 1, 1, "max", None, True, 1.0, 0, "normal"),
+    (1, 1, 1, "softmax", 1, 1, "max", "normal", False, 1.0, 0, "normal"),
+    (67, 256, 8, "sigmoid", 8, 4, "top2", "ties", True, 2.5, 0, "ties"),
+    (67, 256, 8, "softmax", 8, 3, "max", None, False, 1.0, 0, "ties"),
+    (33, 64, 6, "softmax", 1, 1, "max", None, True, 1.0, 0, "ties"),
+    (33, 64, 6, "softmax", 4, 2, "top2", None, True, 1.0, 0, "normal"),
+    (50, 72, 4, "sigmoid", 8, 2, "top2", None, False, 1.5, 0, "normal"),
+    (50, 72, 4, "softmax", 8, 5, "top2", "out", False, 1.0, 0, "masked"),
+    (41, 160, 6, "softmax", 8, 3, "max", "normal", True, 16.0, 0, "masked"),
+    (41, 160, 6, "sigmoid", 1, 1, "max", "out", True, 1.0, 7, "masked"),
+    (19, 128, 32, "sigmoid", 1, 1, "max", "ties", True, 1.0, 0, "wide"),
+    (19, 128, 8, "sigmoid", 16, 4, "top2", "normal", True, 1.0, 0, "wide"),
+    (19, 128, 8, "softmax", 1, 1, "max", None, False, 1.0, 0, "wide"),
+    (23, 64, 2, "sigmoid", 64, 5, "top2", "normal", True, 1.0, 0, "masked"),  # groups of one
+    (23, 100, 3, "sigmoid", 50, 7, "top2", None, True, 1.0, 0, "ties"),
+    (13, 384, 8, "sigmoid", 1, 1, "max", "normal", True, 2.5, 0, "normal"),
+    (13, 512, 8, "sigmoid", 8, 4, "top2", "normal", True, 2.5, 0, "ties"),
+    (9, 1000, 10, "softmax", 10, 3, "top2", "normal", False, 1.0, 0, "masked"),
+    (9, 1024, 32, "sigmoid", 64, 9, "top2", "out", True, 1.0, 0, "normal"),
+    (300, 48, 4, "softmax", 1, 1, "max", "normal", True, 1.0, 11, "ties"),
+    (300, 48, 4, "sigmoid", 4, 2, "top2", None, False, 2.5, 20, "normal"),
+]
+
+
+def setup(c, seed=5):
+    T, E, k, kind, G, taken, gs, b, renorm, scale, cap, lk = c
+    m = moe()
+    p = m.Problem(T=T, H=64, E=E, k=k, I=64, capacity=cap, renormalize=int(renorm))
+    sc = m.Scoring(kind, G, taken, gs, scale)
+    x, bias = make_logits(T, E, seed, lk), make_bias(E, seed, b)
+    want = scored.route(numpy_of(x), k, kind, capacity=cap, bias=numpy_of(bias), n_group=G,
+                        topk_group=taken, group_score=gs, renorm=renorm, scale=scale)
+    return m, p, sc, x, bias, want
+
+
+@pytest.mark.parametrize("c", CASES, ids=str)
+def test_route_scored(c):
+    m, p, sc, x, bias, (ids, w, keep) = setup(c)
+    got = m.route_scored(p, x.cuda(), sc, bias=None if bias is None else bias.cuda())
+    assert not (got[0].cpu().numpy() != ids).any()
+    assert not (got[2].cpu().numpy() != keep).any()
+    # a weight is an fp64 value (off by a few 2^-53) rounded to f32: half a step, 2^-24, of itself
+    # from the other's where the two lie on different sides of a border: a whole step
+    err = np.abs(got[1].cpu().numpy().astype(np.float64) - w)
+    assert (err <= 2.0 ** -23 * np.abs(w) + 2.0 ** -149).all()
+
+
+@pytest.mark.parametrize("c", CASES, ids=str)
+def test_backward(c):
+    m, p, sc, x, bias, (ids, w, keep) = setup(c)
+    dw = torch.randn(p.T, p.k, generator=torch.Generator().manual_seed(9))
+    dw[torch.from_numpy(keep) == 0] = 0
+    dw[torch.from_numpy(w) == 0] = float("nan")  # slots without a weight are not read
+    want, size = scored.backward(numpy_of(x), ids, w, numpy_of(dw), sc.score, bool(p.renormalize),
+                                 sc.scale)
+    got = m.route_scored_backward(p, x.cuda(), sc, torch.from_numpy(ids).cuda(),
+                                  torch.from_numpy(w).cuda(), dw.cuda()).cpu().double().numpy()
+    # the weights were rounded to f32 (2^-24 of themselves each, which moves every term by as
+    # much, and a mean of terms by twice that), the result once more (2^-24); a weight below the
+    # normal range is off by 2^-150
+    g = np.nan_to_num(np.abs(dw.numpy())).sum(1, keepdims=True)
+    tol = 4 * 2.0 ** -24 * size + 2.0 ** -24 * np.abs(want) + 2.0 ** -149 * (1 + 4 * g)
+    assert np.isfinite(got).all()
+    assert (np.abs(got - want) <= tol).all()
+    assert (got[~(numpy_of(x) > -INF)] == 0).all()
+
+
+def test_router_scored_selects_from_its_own_logits():
+    m = moe()
+    T, H, E, k = 300, 192, 96, 6
+    g = torch.Generator().manual_seed(1)
+    x = torch.randn(T, H, generator=g).bfloat16()
+    wr = (torch.randn(E, H, generator=g) * H ** -0.5).bfloat16()
+    b = make_bias(E, 4)
+    for cap in (0, 15):
+        p = m.Problem(T=T, H=H, E=E, k=k, I=64, capacity=cap)
+        sc = m.Scoring("sigmoid", 8, 3, "top2", 2.5)
+        ids, w, keep, lg = m.router_scored(p, x.cuda(), wr.cuda(), sc, bias=b.cuda(),
+                                           want_logits=True)
+        ref = x.double() @ wr.double().t()
+        size = x.double().abs() @ wr.double().abs().t()
+        assert ((lg.cpu().double() - ref).abs() <= 2 * H * 2.0 ** -24 * size).all()
+        want = scored.route(lg.cpu().numpy(), k, "sigmoid", capacity=cap, bias=numpy_of(b),
+                            n_group=8, topk_group=3, group_score="top2", scale=2.5)
+        assert np.array_equal(ids.cpu().numpy(), want[0])
+        assert np.array_equal(keep.cpu().numpy(), want[2])
+        same = m.route_scored(p, lg, sc, bias=b.cuda())
+        assert all(torch.equal(a, q) for a, q in zip((ids, w, keep), same))
+        none = m.router_scored(p, x.cuda(), wr.cuda(), sc, bias=b.cuda())
+        assert none[3] is None and torch.equal(none[0], ids)
+
+
+def test_softmax_without_bias_is_route_grouped():
+    m = moe()
+    T, E, k = 500, 128, 8
+    x = make_logits(T, E, 8, "ties").cuda()
+    p = m.Problem(T=T, H=64, E=E, k=k, I=64, capacity=40)
+    a = m.route_grouped(p, x, 8, 3)
+    b = m.route_scored(p, x, m.Scoring("softmax", 8, 3, "max"))
+    assert torch.equal(a[0], b[0])
+    assert ((a[1] - b[1]).abs() <= 1e-6 * b[1]).all()
+
+
+def test_large_batch_capture_and_streams():
+    """A captured call replayed on new logits, and the call on another stream."""
+    m = moe()
+    T, E, k = 5000, 256, 8
+    p = m.Problem(T=T, H=64, E=E, k=k, I=64, capacity=200)
+    sc = m.Scoring("sigmoid", 8, 4, "top2", 2.5)
+    b = make_bias(E, 2).cuda()
+    x = make_logits(T, E, 3).cuda()
+    ws = m.workspace(p, m.OP_ROUTE)
+    dw = torch.randn(T, k, device="cuda")
+    out = (torch.empty(T, k, dtype=torch.int32, device="cuda"),
+           torch.empty(T, k, device="cuda"), torch.empty(T, k, dtype=torch.uint8, device="cuda"))
+    dl = torch.empty(T, E, device="cuda")
+
+    def call():
+        m.route_scored(p, x, sc, bias=b, out=out, ws=ws)
+        m.route_scored_backward(p, x, sc, out[0], out[1], dw, out=dl)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        call()
+    torch.cuda.current_stream().wait_stream(side)
+    first = [t.clone() for t in (*out, dl)]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for seed in (3, 11, 12):
+        x.copy_(make_logits(T, E, seed))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in (*out, dl)]
+        call()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, q) for a, q in zip(got, (*out, dl)))
+        if seed == 3:
+            assert all(torch.equal(a, q) for a, q in zip(got, first))
