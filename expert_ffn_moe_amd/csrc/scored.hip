@@ -6,9 +6,14 @@
 //   order   s + b, or the logits themselves without a bias (the scores rise with them)
 //   weight  c s / (sum of the chosen s), or c s
 //
-// Choices are made and weights computed in 64 bits and each weight is rounded once: a choice
-// next to a border, and the capacity's comparison of weights, do then not depend on how an
-// exponential was rounded to 32 bits.
+// Choices are those of 64-bit scores and weights are computed in 64 bits and rounded once: a
+// choice next to a border, and the capacity's comparison of weights, do then not depend on how an
+// exponential was rounded to 32 bits.  Most choices are nowhere near a border: a token is first
+// taken in 32 bits, and again in 64 only where two of the values that decided lay closer than
+// their error bounds (or were equal, or an expert that is out would be needed).
+#include <algorithm>
+#include <initializer_list>
+
 #include "moe_internal.h"
 #include "scored.h"
 #include "wave.h"
@@ -25,10 +30,13 @@ struct ScoredArgs {
   uint8_t* keep;
   size_t plane;
   int S, T, E, k, renorm, score, n_group, topk_group, group_score;
+  int vec;   // rows can be read in words of min(EPL, 4) values
+  int span;  // rows kernel: lanes of a group where it is 2^n whole lanes, else 0
   double scale;
 };
 
 constexpr float kBig = 3.402823466e38f;
+constexpr float kLog2e = 1.4426950408889634f;
 
 // Order-preserving map of fp64 (with -0 folded into +0) to uint64; every number maps above 1.
 __device__ __forceinline__ uint64_t ordered_bits(double v) {
@@ -36,154 +44,483 @@ __device__ __forceinline__ uint64_t ordered_bits(double v) {
   return (u >> 63) ? ~u : (u | 0x8000000000000000ull);
 }
 
+constexpr int kDppRowNext = 0x101;  // row_shl:1: the next lane of the row (0 behind the last)
+
+template <int CTRL>
+__device__ __forceinline__ float dpp_f(float v) {
+  return __uint_as_float(dpp_u32<CTRL>(__float_as_uint(v)));
+}
 __device__ __forceinline__ double wave_sum(double v) {
 #pragma unroll
   for (int d = 32; d >= 1; d >>= 1) v += __shfl_xor(v, d, 64);
   return v;
 }
+// Over the 16 lanes of a row, the same in each.
+__device__ __forceinline__ float row_sum(float v) {
+  v += dpp_f<kDppQuadXor1>(v);
+  v += dpp_f<kDppQuadXor2>(v);
+  v += dpp_f<kDppRowHalfMirror>(v);
+  return v + dpp_f<kDppRowMirror>(v);
+}
+template <int CTRL>
+__device__ __forceinline__ double dpp_d(double v) {
+  return __builtin_bit_cast(double, dpp_u64<CTRL>(__builtin_bit_cast(uint64_t, v)));
+}
+__device__ __forceinline__ double row_sum(double v) {
+  v += dpp_d<kDppQuadXor1>(v);
+  v += dpp_d<kDppQuadXor2>(v);
+  v += dpp_d<kDppRowHalfMirror>(v);
+  return v + dpp_d<kDppRowMirror>(v);
+}
+__device__ __forceinline__ float from_lane(float v, int src) {
+  return __uint_as_float(__builtin_amdgcn_ds_bpermute(4 * src, (int)__float_as_uint(v)));
+}
+__device__ __forceinline__ float row_max(float v) {
+  v = fmaxf(v, dpp_f<kDppQuadXor1>(v));
+  v = fmaxf(v, dpp_f<kDppQuadXor2>(v));
+  v = fmaxf(v, dpp_f<kDppRowHalfMirror>(v));
+  return fmaxf(v, dpp_f<kDppRowMirror>(v));
+}
+__device__ __forceinline__ uint32_t row_top(uint32_t v) {
+  v = max(v, dpp_u32<kDppQuadXor1>(v));
+  v = max(v, dpp_u32<kDppQuadXor2>(v));
+  v = max(v, dpp_u32<kDppRowHalfMirror>(v));
+  return max(v, dpp_u32<kDppRowMirror>(v));
+}
 __device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) v = fmaxf(v, __shfl_xor(v, d, 64));
-  return v;
+  v = fmaxf(v, dpp_f<kDppQuadXor1>(v));
+  v = fmaxf(v, dpp_f<kDppQuadXor2>(v));
+  v = fmaxf(v, dpp_f<kDppRowHalfMirror>(v));
+  v = fmaxf(v, dpp_f<kDppRowMirror>(v));
+  v = fmaxf(v, __shfl_xor(v, 16, 64));
+  return fmaxf(v, __shfl_xor(v, 32, 64));
+}
+// Order-preserving map of fp32 to uint32 and back.
+__device__ __forceinline__ uint32_t ordered32(float v) {
+  const uint32_t u = __float_as_uint(v);
+  return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float unordered32(uint32_t o) {
+  return __uint_as_float(o ^ ((uint32_t)(~(int32_t)o >> 31) | 0x80000000u));
+}
+constexpr uint32_t kOutKey = 0x007FFFFFu;  // of -inf
+
+// exp(x) for x <= 0 in 64 bits: x = n ln 2 + r, |r| <= ln 2 / 2, the Taylor series of exp(r) to
+// r^13 (the next term is below 2^-57 of it), times 2^n.
+__device__ __forceinline__ double exp64(double x) {
+  x = fmax(x, -1000.0);  // 0 from there on; -inf
+  const double n = rint(x * 1.4426950408889634);
+  // ln 2 as 0x1.62e42fee p-1 (n times it is exact) and the rest
+  double r = fma(n, -0x1.62e42feep-1, x);
+  r = fma(n, -0x1.a39ef35793c76p-33, r);
+  double q = 1.0 / 6227020800.0;
+  q = fma(q, r, 1.0 / 479001600.0);
+  q = fma(q, r, 1.0 / 39916800.0);
+  q = fma(q, r, 1.0 / 3628800.0);
+  q = fma(q, r, 1.0 / 362880.0);
+  q = fma(q, r, 1.0 / 40320.0);
+  q = fma(q, r, 1.0 / 5040.0);
+  q = fma(q, r, 1.0 / 720.0);
+  q = fma(q, r, 1.0 / 120.0);
+  q = fma(q, r, 1.0 / 24.0);
+  q = fma(q, r, 1.0 / 6.0);
+  q = fma(q, r, 0.5);
+  q = fma(q, r, 1.0);
+  q = fma(q, r, 1.0);
+  return ldexp(q, (int)n);
+}
+// 1 / (1 + exp(-x))
+__device__ __forceinline__ double sigmoid64(double x) {
+  const double e = exp64(-fabs(x));
+  return (x >= 0.0 ? 1.0 : e) / (1.0 + e);
 }
 
 // NaN and -inf, as a logit or a bias: the expert is out; +inf counts as the largest number.
 __device__ __forceinline__ bool is_in(float v) { return v > -INFINITY; }
+__device__ __forceinline__ float tamed(float v) { return is_in(v) ? fminf(v, kBig) : -INFINITY; }
 
-// One wavefront per token; a lane holds experts lane, lane + 64, ...
-template <int EPL>  // E <= 64 * EPL
-__global__ __launch_bounds__(256) void scored_kernel(const ScoredArgs a) {
-  __shared__ double s_val[4][64 * EPL];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int t = blockIdx.x * 4 + wave;
-  if (t >= a.T) return;  // wave-uniform
+// Values EPL lane .. EPL lane + EPL - 1 of a row of E; fill behind its end.
+template <int EPL>
+__device__ __forceinline__ void load_row(const float* row, int E, int lane, bool vec, float fill,
+                                         float (&v)[EPL]) {
+  constexpr int W = EPL < 4 ? EPL : 4;
+  typedef float word __attribute__((ext_vector_type(W)));
+  if (vec) {  // uniform
+#pragma unroll
+    for (int i = 0; i < EPL; i += W) {
+      word q;
+#pragma unroll
+      for (int j = 0; j < W; ++j) q[j] = fill;
+      if (lane * EPL + i < E) q = *(const word*)(row + lane * EPL + i);
+#pragma unroll
+      for (int j = 0; j < W; ++j) v[i + j] = q[j];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) v[i] = lane * EPL + i < E ? row[lane * EPL + i] : fill;
+  }
+}
+
+// The logits of token t, planes added in order.
+template <int EPL>
+__device__ __forceinline__ void load_logits(const ScoredArgs& a, int t, int lane, float (&l)[EPL]) {
   const float* row = a.logits + (size_t)t * a.E;
-  float l[EPL];
-  bool in[EPL], can[EPL];  // part of the softmax; to be chosen
-  double c[EPL];           // what the experts are ordered by
+  load_row<EPL>(row, a.E, lane, a.vec, -INFINITY, l);
+  for (int p = 1; p < a.S; ++p) {
+    float v[EPL];
+    load_row<EPL>(row + p * a.plane, a.E, lane, a.vec, 0.0f, v);
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) l[i] += v[i];
+  }
+}
+
+// The two largest of the disjoint sets of two lanes.
+__device__ __forceinline__ void merge2(float& a1, float& a2, float b1, float b2) {
+  a2 = fmaxf(fminf(a1, b1), fmaxf(a2, b2));
+  a1 = fmaxf(a1, b1);
+}
+
+// The k choices of token t in 64 bits by one wavefront, a lane holding EPL consecutive experts:
+// lane j returns the expert of slot j.  s_val: 64 EPL values of this wavefront's own.
+template <int EPL>
+__device__ __forceinline__ int choose64(const ScoredArgs& a, int t, int lane, double* s_val) {
+  const bool softmax = a.score == MOE_SCORE_SOFTMAX;
+  const bool grouped = a.n_group > 1 && a.topk_group < a.n_group;
+  const bool top2 = grouped && a.group_score == MOE_GROUP_TOP2;
+  float l[EPL], b[EPL];
+  load_logits<EPL>(a, t, lane, l);
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) b[i] = 0.0f;
+  if (a.bias) load_row<EPL>(a.bias, a.E, lane, a.vec, -INFINITY, b);
+  float m = -kBig;
+  double total = 0.0, d[EPL];
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
-    const int e = lane + 64 * i;
-    float v = -INFINITY;
-    if (e < a.E) {
-      v = row[e];
-#pragma unroll 8
-      for (int q = 1; q < a.S; ++q) v = v + row[q * a.plane + e];
-      if (a.logits_out) a.logits_out[(size_t)t * a.E + e] = v;
-    }
-    in[i] = is_in(v);
-    can[i] = in[i] && (!a.bias || is_in(a.bias[e]));
-    l[i] = fminf(v, kBig);
-    c[i] = l[i];
+    l[i] = tamed(l[i]);
+    b[i] = tamed(b[i]);
+    m = fmaxf(m, l[i]);
+    d[i] = 0.0;
   }
-  const bool grouped = a.n_group > 1 && a.topk_group < a.n_group;
-  const bool by_score = grouped && a.group_score == MOE_GROUP_TOP2;
-  const bool softmax = a.score == MOE_SCORE_SOFTMAX;
-  float m = 0.0f;
-  double total = 1.0;  // of the softmax over all experts
-  if (softmax) {
-    m = -kBig;
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) m = in[i] ? fmaxf(m, l[i]) : m;
-    m = wave_max(m);
-  }
-  auto score_of = [&](float v) {
-    return softmax ? exp((double)v - (double)m) : 1.0 / (1.0 + exp(-(double)v));
-  };
-  double s[EPL];
-  const bool all = a.bias || by_score || (softmax && !a.renorm);
-  if (all) {
-    total = 0.0;
+  m = wave_max(m);
+  if (a.bias || top2) {
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
-      s[i] = in[i] ? score_of(l[i]) : 0.0;
-      total += s[i];
+      d[i] = !is_in(l[i]) ? 0.0
+             : softmax    ? exp64((double)l[i] - (double)m)
+                          : sigmoid64(l[i]);
+      total += d[i];
     }
     total = softmax ? wave_sum(total) : 1.0;
     if (!(total > 0.0)) total = 1.0;
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-      s[i] /= total;
-      if (a.bias && lane + 64 * i < a.E) {
-        s[i] += (double)fminf(a.bias[lane + 64 * i], kBig);
-        c[i] = s[i];
-      }
-    }
   }
   // 0: not to be chosen, 1: out (chosen last, lowest id first), else the order
   uint64_t key[EPL];
 #pragma unroll
-  for (int i = 0; i < EPL; ++i)
-    key[i] = lane + 64 * i >= a.E ? 0 : can[i] ? ordered_bits(c[i]) : 1;
+  for (int i = 0; i < EPL; ++i) {
+    const bool can = is_in(l[i]) && is_in(b[i]);
+    if (a.bias || top2) d[i] = d[i] / total + (double)(can ? b[i] : 0.0f);
+    const double by = a.bias ? d[i] : (double)l[i];
+    key[i] = lane * EPL + i >= a.E ? 0 : can ? ordered_bits(by) : 1;
+    if (grouped) s_val[lane * EPL + i] = can ? (top2 ? d[i] : by) : -INFINITY;
+  }
   if (grouped) {
     const int gs = a.E / a.n_group;
-#pragma unroll
-    for (int i = 0; i < EPL; ++i)
-      s_val[wave][lane + 64 * i] = can[i] ? (by_score ? s[i] : c[i]) : -INFINITY;
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");  // this wavefront's own values
     __builtin_amdgcn_wave_barrier();
     uint64_t g = 0;
     if (lane < a.n_group) {
       double v1 = -INFINITY, v2 = -INFINITY;
-      for (int q = 0; q < gs; ++q) {
-        const double v = s_val[wave][lane * gs + q];
+      for (int o = 0; o < gs; ++o) {
+        const double v = s_val[lane * gs + o];
         v2 = fmax(v2, fmin(v1, v));
         v1 = fmax(v1, v);
       }
-      if (by_score && v2 > -INFINITY) v1 += v2;
+      if (top2 && v2 > -INFINITY) v1 += v2;
       g = ordered_bits(v1);
     }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();  // before the next token's values
     int ahead = 0;
-    for (int q = 0; q < a.n_group; ++q) {
-      const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)g, q);
-      const uint32_t hi = __builtin_amdgcn_readlane((uint32_t)(g >> 32), q);
-      const uint64_t o = ((uint64_t)hi << 32) | lo;
-      ahead += o > g || (o == g && q < lane);
+    for (int o = 0; o < a.n_group; ++o) {
+      const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)g, o);
+      const uint32_t hi = __builtin_amdgcn_readlane((uint32_t)(g >> 32), o);
+      const uint64_t v = ((uint64_t)hi << 32) | lo;
+      ahead += v > g || (v == g && o < lane);
     }
     const uint64_t taken = __ballot(lane < a.n_group && ahead < a.topk_group);
 #pragma unroll
     for (int i = 0; i < EPL; ++i)
-      if (lane + 64 * i < a.E && !((taken >> ((lane + 64 * i) / gs)) & 1)) key[i] = 0;
+      if (lane * EPL + i < a.E && !((taken >> ((lane * EPL + i) / gs)) & 1)) key[i] = 0;
   }
-  // k rounds of a maximum; equal keys: the lowest expert
-  int my_e = 0;
-  float my_l = 0.0f;
-  bool my_in = false;
+  int mine = 0;
   for (int j = 0; j < a.k; ++j) {
     uint64_t best = key[0];
 #pragma unroll
     for (int i = 1; i < EPL; ++i) best = max_u64(best, key[i]);
     best = wave_max_u64(best);
-    int e = 0;
-    float v = 0.0f;
-    bool found = false;
+    // equal keys: the lowest expert, in the lowest lane and there the lowest of its values
+    uint64_t any = 0;
+    int place = EPL;
+#pragma unroll
+    for (int i = EPL - 1; i >= 0; --i) {
+      const bool hit = key[i] == best;
+      any |= __ballot(hit);
+      place = hit ? i : place;
+    }
+    const int src = __builtin_ctzll(any);
+    const int at = __builtin_amdgcn_readlane(place, src);
+#pragma unroll
+    for (int i = 0; i < EPL; ++i)
+      if (lane == src && i == at) key[i] = 0;
+    mine = lane == j ? src * EPL + at : mine;
+  }
+  return mine;
+}
+
+// The weight of expert e of token t before scale and renormalisation, 0 where it is out (m, total:
+// the softmax's), and whether it is in.
+__device__ __forceinline__ double weight_of(const ScoredArgs& a, int t, int e, float m,
+                                            double total, bool& in) {
+  const float* at = a.logits + (size_t)t * a.E + e;
+  float l = *at;
+  for (int p = 1; p < a.S; ++p) l += at[p * a.plane];
+  l = tamed(l);
+  in = is_in(l) && (!a.bias || is_in(a.bias[e]));
+  if (!in) return 0.0;
+  return a.score == MOE_SCORE_SOFTMAX ? exp64((double)l - (double)m) / total : sigmoid64(l);
+}
+
+__device__ __forceinline__ void order2(uint32_t& a, uint32_t& b) {  // the larger first
+  const uint32_t hi = max(a, b);
+  b = min(a, b);
+  a = hi;
+}
+// Sorts 4 or 8 keys, largest first (odd-even merging).
+template <int N>
+__device__ __forceinline__ void sort_keys(uint32_t* v) {
+  if constexpr (N == 4) {
+    order2(v[0], v[1]); order2(v[2], v[3]);
+    order2(v[0], v[2]); order2(v[1], v[3]);
+    order2(v[1], v[2]);
+  } else {
+    sort_keys<4>(v);
+    sort_keys<4>(v + 4);
+    order2(v[0], v[4]); order2(v[1], v[5]); order2(v[2], v[6]); order2(v[3], v[7]);
+    order2(v[2], v[4]); order2(v[3], v[5]);
+    order2(v[1], v[2]); order2(v[3], v[4]); order2(v[5], v[6]);
+  }
+}
+
+// A row of 16 lanes takes a token, a lane EPL consecutive experts: four tokens to a wavefront, every
+// reduction inside a row.  Each lane sorts its keys first, so that a round of the choice is the
+// maximum of the lanes' heads and the winner moves on to its next one.  For k <= 8.
+//
+// In 32 bits a key is the order-preserving bits of the value, the last ones replaced by the value's
+// place in its lane.  Bounds: a sigmoid from the hardware's exponential and reciprocal (1 ulp
+// each) is off by at most 2^-22 (|l| s (1 - s) < 0.23 times the argument's rounding, 2^-24 for the
+// sum, 2^-23 for the reciprocal), with the bias 2^-24 of the sum more; a softmax by at most 2^-19
+// (its total by 25 2^-24 of itself).  Two values are told apart where they differ by more than
+// the sum of their bounds, taken as eps (1 + |value|) with eps 2^-20 (2^-17 for the softmax) and
+// EPL 2^-22 |value| for the keys, group values of two scores with twice the first.
+template <int EPL, bool SOFTMAX>  // E <= 16 * EPL
+__global__ __launch_bounds__(256) void scored_rows_kernel(const ScoredArgs a) {
+  constexpr int D = EPL < 8 ? EPL : 8;  // keys a lane keeps
+  constexpr int kWide = EPL / 4;        // experts per lane where the wavefront takes one token
+  __shared__ double s_val[4][64 * kWide];
+  __shared__ int s_e[4][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l16 = lane & 15;
+  const int t0 = (blockIdx.x * 4 + wave) * 4;
+  if (t0 >= a.T) return;  // wave-uniform
+  const int t = min(t0 + (lane >> 4), a.T - 1);
+  const bool live = t0 + (lane >> 4) < a.T;
+  const bool grouped = a.n_group > 1 && a.topk_group < a.n_group;
+  const bool top2 = grouped && a.group_score == MOE_GROUP_TOP2;
+  const bool scores = a.bias || top2;
+  const float eps = SOFTMAX ? 0x1p-17f : 0x1p-20f;
+
+  float l[EPL];
+  load_logits<EPL>(a, t, l16, l);
+  if (a.logits_out && live) {
+#pragma unroll
+    for (int i = 0; i < EPL; ++i)
+      if (l16 * EPL + i < a.E) a.logits_out[(size_t)t * a.E + l16 * EPL + i] = l[i];
+  }
+  float m = -kBig;
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) l[i] = tamed(l[i]);
+  if constexpr (SOFTMAX) {
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) m = fmaxf(m, l[i]);
+    m = row_max(m);
+  }
+  float s[EPL], c[EPL];  // the scores, and what the experts are ordered by
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) s[i] = c[i] = l[i];
+  if (scores) {
+    float f = 1.0f;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i)
+      s[i] = SOFTMAX ? __builtin_amdgcn_exp2f((l[i] - m) * kLog2e)
+                     : __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(l[i] * -kLog2e));
+    if constexpr (SOFTMAX) {
+      f = s[0];
+#pragma unroll
+      for (int i = 1; i < EPL; ++i) f += s[i];
+      f = row_sum(f);
+      f = f > 0.0f ? __builtin_amdgcn_rcpf(f) : 0.0f;
+    }
+    float b[EPL];
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) b[i] = 0.0f;
+    if (a.bias) load_row<EPL>(a.bias, a.E, l16, a.vec, -INFINITY, b);
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
-      const uint64_t at = __ballot(key[i] == best);
-      if (!found && at) {  // wave-uniform
-        const int src = __builtin_ctzll(at);
-        e = src + 64 * i;
-        v = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(l[i]), src));
-        if (lane == src) key[i] = 0;
-        found = true;
-      }
-    }
-    if (lane == j) {
-      my_e = e;
-      my_l = v;
-      my_in = best > 1;
+      // (as a sum: for a choice between two values the compiler branches around the exponential)
+      s[i] = fmaf(s[i], f, tamed(b[i])) + (is_in(l[i]) ? 0.0f : -INFINITY);
+      c[i] = a.bias ? s[i] : c[i];
     }
   }
-  double w = lane < a.k && my_in ? score_of(my_l) / total : 0.0;
+  bool unsure = grouped && a.span == 0;
+  if (grouped && a.span != 0) {
+    float v1 = -INFINITY, v2 = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      const float v = top2 ? s[i] : c[i];
+      v2 = fmaxf(v2, fminf(v1, v));
+      v1 = fmaxf(v1, v);
+    }
+    if (a.span > 1) merge2(v1, v2, dpp_f<kDppQuadXor1>(v1), dpp_f<kDppQuadXor1>(v2));
+    if (a.span > 2) merge2(v1, v2, dpp_f<kDppQuadXor2>(v1), dpp_f<kDppQuadXor2>(v2));
+    if (a.span > 4) merge2(v1, v2, dpp_f<kDppRowHalfMirror>(v1), dpp_f<kDppRowHalfMirror>(v2));
+    const float mine = top2 && is_in(v2) ? v1 + v2 : v1;
+    // (ordered by the logits themselves only equal groups are close)
+    const float near = scores ? 2.0f * eps * (1.0f + fabsf(mine)) : 0.0f;
+    int ahead = 0, close = 0;
+    for (int o = 0; o < a.n_group; ++o) {
+      const float v = from_lane(mine, (lane & 48) + o * a.span);
+      ahead += v > mine;
+      close += fabsf(v - mine) <= near;
+    }
+    unsure = close > 1 && l16 < a.n_group * a.span;  // (each is close to itself)
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) c[i] = ahead < a.topk_group ? c[i] : -INFINITY;
+  }
+  uint32_t key[EPL];
+#pragma unroll
+  for (int i = 0; i < EPL; ++i)
+    key[i] = (ordered32(c[i]) & ~(uint32_t)(EPL - 1)) | (uint32_t)(EPL - 1 - i);
+  if constexpr (EPL == 16) {  // the larger half, again in order
+    sort_keys<8>(key);
+    sort_keys<8>(key + 8);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) key[i] = max(key[i], key[15 - i]);
+#pragma unroll
+    for (int d = 4; d >= 1; d >>= 1)
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (!(i & d)) order2(key[i], key[i + d]);
+  } else {
+    sort_keys<EPL>(key);
+  }
+  uint32_t tops = 0, last = 0;  // lane j of a row: the key of round j; the first not chosen
+  uint64_t twice = 0;           // rows in which two lanes had the same key
+  for (int j = 0;; ++j) {
+    last = row_top(key[0]);
+    if (j == a.k) break;
+    const bool win = key[0] == last;
+    const uint64_t who = __ballot(win);
+    twice |= who & (who - 0x0001000100010001ull);  // (each row has a winner)
+    tops = l16 == j ? last : tops;
+    if (win) s_e[wave][(lane & 48) + j] = l16 * EPL + (EPL - 1 - (int)(last & (EPL - 1)));
+    // (as bits: the compiler made selects of the keys an indexed array, 190 instructions a round)
+    const uint32_t next = win ? ~0u : 0u;
+#pragma unroll
+    for (int i = 0; i < D; ++i)
+      key[i] = (next & (i + 1 < D ? key[i + 1] : 0)) | (~next & key[i]);
+  }
+  uint32_t after = dpp_u32<kDppRowNext>(tops);
+  after = l16 == a.k - 1 ? last : after;
+  const float v = unordered32(tops), w1 = unordered32(after);
+  const float apart = (a.bias ? eps : 0x1p-126f) +
+                      ((a.bias ? eps : 0.0f) + EPL * 0x1p-22f) * fmaxf(fabsf(v), fabsf(w1));
+  // (out: fewer than k can be chosen; the first that is not chosen may be)
+  unsure = unsure || (l16 < a.k && (tops <= kOutKey || (after > kOutKey && v - w1 <= apart))) ||
+           (EPL > D && key[0] == 0);  // a lane whose next key is not known
+  uint64_t again = (__ballot(unsure && live) | twice) & __ballot(live);
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  int e = s_e[wave][lane];
+  for (int r = 0; r < 4; ++r) {
+    if (!((again >> (16 * r)) & 0xFFFF)) continue;  // wave-uniform
+    int lane_v = lane;  // through an empty statement: nothing of this is computed ahead
+    asm volatile("" : "+v"(lane_v));
+    const int got = __shfl(choose64<kWide>(a, t0 + r, lane_v, s_val[wave]), lane & 15, 64);
+    e = lane >> 4 == r ? got : e;
+  }
+  double total = 1.0;
+  if (SOFTMAX && !a.renorm) {
+    total = 0.0;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) total += exp64((double)l[i] - (double)m);
+    total = row_sum(total);
+    if (!(total > 0.0)) total = 1.0;
+  }
+  bool in = false;
+  double w = l16 < a.k ? weight_of(a, t, e, m, total, in) : 0.0;
+  if (a.renorm) {
+    const double sum = row_sum(w);
+    w = sum > 0.0 ? w / sum : 0.0;
+  }
+  if (live && l16 < a.k) {
+    const size_t o = (size_t)t * a.k + l16;
+    a.ids[o] = e;
+    a.w[o] = (float)(a.scale * w);
+    a.keep[o] = in;
+  }
+}
+
+// A wavefront per token, for more experts or choices; in 64 bits throughout.
+template <int EPL>  // E <= 64 * EPL
+__global__ __launch_bounds__(256) void scored_wide_kernel(const ScoredArgs a) {
+  __shared__ double s_val[4][64 * EPL];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int t = blockIdx.x * 4 + wave;
+  if (t >= a.T) return;  // wave-uniform
+  const bool softmax = a.score == MOE_SCORE_SOFTMAX;
+  float m = 0.0f;
+  double total = 1.0;
+  if (softmax || a.logits_out) {
+    float l[EPL];
+    load_logits<EPL>(a, t, lane, l);
+    m = -kBig;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      if (a.logits_out && lane * EPL + i < a.E)
+        a.logits_out[(size_t)t * a.E + lane * EPL + i] = l[i];
+      l[i] = tamed(l[i]);
+      m = fmaxf(m, l[i]);
+    }
+    m = wave_max(m);
+    if (softmax && !a.renorm) {
+      total = 0.0;
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) total += exp64((double)l[i] - (double)m);
+      total = wave_sum(total);
+      if (!(total > 0.0)) total = 1.0;
+    }
+  }
+  const int e = choose64<EPL>(a, t, lane, s_val[wave]);
+  bool in = false;
+  double w = lane < a.k ? weight_of(a, t, e, m, total, in) : 0.0;
   if (a.renorm) {
     const double sum = wave_sum(w);
     w = sum > 0.0 ? w / sum : 0.0;
   }
   if (lane < a.k) {
     const size_t o = (size_t)t * a.k + lane;
-    a.ids[o] = my_e;
+    a.ids[o] = e;
     a.w[o] = (float)(a.scale * w);
-    a.keep[o] = my_in;
+    a.keep[o] = in;
   }
 }
 
@@ -193,7 +530,7 @@ struct ScoredBwdArgs {
   const float* w;
   const float* dw;
   float* dl;
-  int T, E, k, renorm, score;
+  int T, E, k, renorm, score, tokens, vec;
 };
 
 // The gradient of the logits from that of the weights (the choice itself carries none), with
@@ -202,89 +539,158 @@ struct ScoredBwdArgs {
 //   sigmoid                dl_j = w_j (1 - s_j) d_j
 //   softmax, renormalised  dl_j = w_j (d_j - D)
 //   softmax                dl_e = [e chosen] w_e d_e - p_e sum w d
-// In 64 bits, for d_j - D cancels.  One wavefront per token.
+// In 64 bits, for d_j - D cancels.  A wavefront takes a.tokens tokens: their slots first, one to a
+// lane, then their rows, a lane holding EPL consecutive experts.
 template <int EPL>
 __global__ __launch_bounds__(256) void scored_bwd_kernel(const ScoredBwdArgs a) {
   const int lane = threadIdx.x & 63;
-  const int t = blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (t >= a.T) return;  // wave-uniform
-  const float* row = a.logits + (size_t)t * a.E;
-  const size_t o = (size_t)t * a.k;
-  const bool mine = lane < a.k;
-  const int e = mine ? a.ids[o + lane] : -1;
-  const double w = mine ? (double)a.w[o + lane] : 0.0;
-  const double d = mine && w != 0.0 ? (double)a.dw[o + lane] : 0.0;
-  double D = wave_sum(w * d);
-  double g = w * d;
-  if (a.renorm) {
-    const double sum = wave_sum(w);
-    D = sum != 0.0 ? D / sum : 0.0;
-    g = w * (d - D);
+  const int t0 = (blockIdx.x * 4 + (threadIdx.x >> 6)) * a.tokens;
+  if (t0 >= a.T) return;  // wave-uniform
+  const int nt = min(a.tokens, a.T - t0);
+  const size_t o = (size_t)t0 * a.k + lane;
+  const bool mine = lane < nt * a.k;
+  const int e = mine ? a.ids[o] : -1;
+  const double w = mine ? (double)a.w[o] : 0.0;
+  const double d = w != 0.0 ? (double)a.dw[o] : 0.0;
+  const int first = lane / a.k * a.k;
+  double D = 0.0, sum = 0.0;
+  if (a.renorm || a.score == MOE_SCORE_SOFTMAX) {
+    for (int j = 0; j < a.k; ++j) {
+      D += __shfl(w * d, first + j, 64);
+      sum += __shfl(w, first + j, 64);
+    }
   }
+  if (a.renorm) D = sum != 0.0 ? D / sum : 0.0;
+  double g = w * (a.renorm ? d - D : d);
   if (a.score == MOE_SCORE_SIGMOID && w != 0.0 && (unsigned)e < (unsigned)a.E)
-    g /= 1.0 + exp((double)fminf(row[e], kBig));
-  double p[EPL];
+    g *= sigmoid64(-(double)fminf(a.logits[(size_t)(t0 + lane / a.k) * a.E + e], kBig));
+  const float gf = (float)g;
+  const bool dense = a.score == MOE_SCORE_SOFTMAX && !a.renorm;
+  for (int q = 0; q < nt; ++q) {
+    const size_t row = (size_t)(t0 + q) * a.E;
+    float v[EPL];
 #pragma unroll
-  for (int i = 0; i < EPL; ++i) p[i] = 0.0;
-  if (a.score == MOE_SCORE_SOFTMAX && !a.renorm) {
-    float l[EPL];
-    float m = -kBig;
+    for (int i = 0; i < EPL; ++i) v[i] = 0.0f;
+    if (dense) {
+      double p[EPL];
+      float l[EPL];
+      load_row<EPL>(a.logits + row, a.E, lane, a.vec, -INFINITY, l);
+      float m = -kBig;
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-      const int q = lane + 64 * i;
-      l[i] = q < a.E ? row[q] : -INFINITY;
-      m = is_in(l[i]) ? fmaxf(m, fminf(l[i], kBig)) : m;
+      for (int i = 0; i < EPL; ++i) {
+        l[i] = tamed(l[i]);
+        m = fmaxf(m, l[i]);
+      }
+      m = wave_max(m);
+      double total = 0.0;
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) {
+        p[i] = exp64((double)l[i] - (double)m);  // (out: -inf, or no expert at all)
+        total += p[i];
+      }
+      total = wave_sum(total);
+      const double f = total > 0.0 ? -__shfl(D, q * a.k, 64) / total : 0.0;
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) p[i] *= f;
+      for (int j = 0; j < a.k; ++j) {
+        const int ej = __builtin_amdgcn_readlane(e, q * a.k + j);
+        const double gj = __shfl(g, q * a.k + j, 64);
+#pragma unroll
+        for (int i = 0; i < EPL; ++i)
+          if (lane * EPL + i == ej) p[i] += gj;
+      }
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) v[i] = (float)p[i];
+    } else {
+      for (int j = 0; j < a.k; ++j) {
+        const int ej = __builtin_amdgcn_readlane(e, q * a.k + j);
+        const float gj = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(gf), q * a.k + j));
+#pragma unroll
+        for (int i = 0; i < EPL; ++i)
+          if (lane * EPL + i == ej) v[i] += gj;
+      }
     }
-    m = wave_max(m);
-    double total = 0.0;
+    constexpr int W = EPL < 4 ? EPL : 4;
+    typedef float word __attribute__((ext_vector_type(W)));
+    if (a.vec) {
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-      p[i] = is_in(l[i]) ? exp((double)fminf(l[i], kBig) - (double)m) : 0.0;
-      total += p[i];
+      for (int i = 0; i < EPL; i += W) {
+        word x;
+#pragma unroll
+        for (int j = 0; j < W; ++j) x[j] = v[i + j];
+        if (lane * EPL + i < a.E) *(word*)(a.dl + row + lane * EPL + i) = x;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < EPL; ++i)
+        if (lane * EPL + i < a.E) a.dl[row + lane * EPL + i] = v[i];
     }
-    total = wave_sum(total);
-    const double f = total > 0.0 ? -D / total : 0.0;
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) p[i] *= f;
   }
-  for (int j = 0; j < a.k; ++j) {
-    const int ej = __builtin_amdgcn_readlane(e, j);
-    const double gj = __shfl(g, j, 64);
-#pragma unroll
-    for (int i = 0; i < EPL; ++i)
-      if (lane + 64 * i == ej) p[i] += gj;
-  }
-#pragma unroll
-  for (int i = 0; i < EPL; ++i)
-    if (lane + 64 * i < a.E) a.dl[(size_t)t * a.E + lane + 64 * i] = (float)p[i];
+}
+
+// Tokens per wavefront: several share the pass over their slots where enough wavefronts remain.
+int tokens_per_wave(const moe_problem& p) {
+  int n = 4;
+  while (n > 1 && (n * p.k > 64 || p.T / n < 4096)) n /= 2;
+  return n;
+}
+bool words_ok(int E, int epl, std::initializer_list<const void*> ptrs) {
+  const int w = std::min(epl, 4);
+  for (const void* q : ptrs)
+    if ((uintptr_t)q % (4 * w) != 0) return false;
+  return E % w == 0;
+}
+int experts_per_lane(int E) {
+  int n = 1;
+  while (64 * n < E) n *= 2;
+  return n;
 }
 
 }  // namespace
 
+#define MOE_BY_EPL(epl, kernel, ...)                                      \
+  do {                                                                    \
+    if ((epl) == 1) hipLaunchKernelGGL(kernel<1>, __VA_ARGS__);           \
+    else if ((epl) == 2) hipLaunchKernelGGL(kernel<2>, __VA_ARGS__);      \
+    else if ((epl) == 4) hipLaunchKernelGGL(kernel<4>, __VA_ARGS__);      \
+    else if ((epl) == 8) hipLaunchKernelGGL(kernel<8>, __VA_ARGS__);      \
+    else hipLaunchKernelGGL(kernel<16>, __VA_ARGS__);                     \
+  } while (0)
+
 hipError_t launch_route_scored(const moe_problem& p, const moe_scoring& sc, const float* logits,
                                int S, const float* bias, float* logits_out, int32_t* ids, float* w,
                                uint8_t* keep, hipStream_t s) {
-  const ScoredArgs a{logits, bias, logits_out, ids, w, keep, (size_t)p.T * p.E, S, p.T, p.E, p.k,
-                     p.renormalize, sc.score, sc.n_group, sc.topk_group, sc.group_score, sc.scale};
-  const dim3 grid(div_up(p.T, 4)), block(256);
-  if (p.E <= 64) hipLaunchKernelGGL(scored_kernel<1>, grid, block, 0, s, a);
-  else if (p.E <= 128) hipLaunchKernelGGL(scored_kernel<2>, grid, block, 0, s, a);
-  else if (p.E <= 256) hipLaunchKernelGGL(scored_kernel<4>, grid, block, 0, s, a);
-  else if (p.E <= 512) hipLaunchKernelGGL(scored_kernel<8>, grid, block, 0, s, a);
-  else hipLaunchKernelGGL(scored_kernel<16>, grid, block, 0, s, a);
+  ScoredArgs a{logits, bias, logits_out, ids, w, keep, (size_t)p.T * p.E, S, p.T, p.E, p.k,
+               p.renormalize, sc.score, sc.n_group, sc.topk_group, sc.group_score, 0, 0, sc.scale};
+  if (p.E <= 256 && p.k <= 8) {
+    const int epl = p.E <= 64 ? 4 : p.E <= 128 ? 8 : 16, gs = p.E / sc.n_group;
+    // (the wavefront-wide form that the kernel falls back to reads smaller words of the same rows)
+    a.vec = words_ok(p.E, 4, {logits, bias});
+    const int span = gs % epl == 0 ? gs / epl : 0;
+    a.span = span == 1 || span == 2 || span == 4 || span == 8 ? span : 0;
+    const dim3 grid(div_up(p.T, 16)), block(256);
+    const bool soft = sc.score == MOE_SCORE_SOFTMAX;
+    if (epl == 4 && soft) hipLaunchKernelGGL((scored_rows_kernel<4, true>), grid, block, 0, s, a);
+    else if (epl == 4) hipLaunchKernelGGL((scored_rows_kernel<4, false>), grid, block, 0, s, a);
+    else if (epl == 8 && soft) hipLaunchKernelGGL((scored_rows_kernel<8, true>), grid, block, 0, s, a);
+    else if (epl == 8) hipLaunchKernelGGL((scored_rows_kernel<8, false>), grid, block, 0, s, a);
+    else if (soft) hipLaunchKernelGGL((scored_rows_kernel<16, true>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((scored_rows_kernel<16, false>), grid, block, 0, s, a);
+  } else {
+    const int epl = experts_per_lane(p.E);
+    a.vec = words_ok(p.E, epl, {logits, bias});
+    MOE_BY_EPL(epl, scored_wide_kernel, dim3(div_up(p.T, 4)), dim3(256), 0, s, a);
+  }
   return hipGetLastError();
 }
 
 hipError_t launch_route_scored_bwd(const moe_problem& p, const moe_scoring& sc,
                                    const float* logits, const int32_t* ids, const float* w,
                                    const float* dw, float* dlogits, hipStream_t s) {
-  const ScoredBwdArgs a{logits, ids, w, dw, dlogits, p.T, p.E, p.k, p.renormalize, sc.score};
-  const dim3 grid(div_up(p.T, 4)), block(256);
-  if (p.E <= 64) hipLaunchKernelGGL(scored_bwd_kernel<1>, grid, block, 0, s, a);
-  else if (p.E <= 128) hipLaunchKernelGGL(scored_bwd_kernel<2>, grid, block, 0, s, a);
-  else if (p.E <= 256) hipLaunchKernelGGL(scored_bwd_kernel<4>, grid, block, 0, s, a);
-  else if (p.E <= 512) hipLaunchKernelGGL(scored_bwd_kernel<8>, grid, block, 0, s, a);
-  else hipLaunchKernelGGL(scored_bwd_kernel<16>, grid, block, 0, s, a);
+  const int epl = experts_per_lane(p.E);
+  const ScoredBwdArgs a{logits, ids, w, dw, dlogits, p.T, p.E, p.k, p.renormalize, sc.score,
+                        tokens_per_wave(p), words_ok(p.E, epl, {logits, dlogits})};
+  MOE_BY_EPL(epl, scored_bwd_kernel, dim3(div_up(p.T, 4 * a.tokens)), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 
