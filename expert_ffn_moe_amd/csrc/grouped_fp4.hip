@@ -26,11 +26,18 @@ __device__ __align__(16) const uint32_t g_zeros[4] = {0, 0, 0, 0};
 // wavefront's 1 KiB at lds (uniform), lane by lane; m0 carries the LDS address and needs one wait
 // state.  (Inline assembly without register outputs: for the builtin the compiler waits for every
 // copy in flight before each LDS read.)
+template <bool ONCE = false>  // with the non-temporal hint
 __device__ __forceinline__ void copy_to_lds(const uint8_t* base, uint32_t off, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
-               :
-               : "v"(off), "s"(base), "s"(lds)
-               : "memory");
+  if constexpr (ONCE)
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1 nt"
+                 :
+                 : "v"(off), "s"(base), "s"(lds)
+                 : "memory");
+  else
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
+                 :
+                 : "v"(off), "s"(base), "s"(lds)
+                 : "memory");
 }
 __device__ __forceinline__ void copy_to_lds(const uint8_t* src, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off"
@@ -76,12 +83,14 @@ __device__ __forceinline__ u32x2 scale_words(const uint8_t* row, int b, int nb) 
   return v;
 }
 
-// One output tile.
+// One output tile, or one part of its reduction.
 struct Item {
-  int e;     // expert
-  int m0;    // first row
-  int rows;  // live rows
-  int n0;    // first output column
+  int e;       // expert
+  int m0;      // first row
+  int rows;    // live rows
+  int n0;      // first output column
+  int part;    // of a split reduction
+  int s0, s1;  // its stages
 };
 
 // Persistent.  A tile is BM rows of x against 64 WN weight rows: 64 WN output columns, or 32 WN of
@@ -97,7 +106,8 @@ struct Item {
 // come through registers (their rows need not be aligned): loaded with a stage's copies, stored
 // before the barrier behind which the stage is read, ordered so that one LDS read brings a lane
 // the words of all its fragments.
-template <bool EIGHT, bool GATHER, int BM, int WM, int WN>
+// ONCE: the weights are read once (one M tile per expert), with the non-temporal hint.
+template <bool EIGHT, bool GATHER, int BM, int WM, int WN, bool ONCE = false>
 __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2, 2)))
 void fp4_tile_kernel(const Fp4Args g) {
   constexpr int NT = 64 * WM * WN, BN = 64 * WN;
@@ -122,7 +132,7 @@ void fp4_tile_kernel(const Fp4Args g) {
   const bool gated = g.up.codes != nullptr;
   const int cols = gated ? BN / 2 : BN;  // output columns of a tile
   const int nb = g.K / 32, nst = div_up(nb, kStageBlocks);
-  const int ntn = div_up(g.N, cols);  // items per M tile
+  const int ntn = div_up(g.N, cols), per_tile = ntn * g.split;  // items per M tile
 
   // ---- the M tiles before each expert, and this XCD's share of the items: an eighth of what they
   // cost in rows, a tile's own time being that of 3/4 of its height more than its rows'
@@ -133,7 +143,7 @@ void fp4_tile_kernel(const Fp4Args g) {
     fp4_segment(g, 0, beg1, end1);
     beg1 = __builtin_amdgcn_readfirstlane(beg1);
     end1 = __builtin_amdgcn_readfirstlane(end1);
-    const int total = div_up(end1 - beg1, BM) * ntn;
+    const int total = div_up(end1 - beg1, BM) * per_tile;
     first = (int)((int64_t)total * xcd / kXcds);
     last = (int)((int64_t)total * (xcd + 1) / kXcds);
   } else {
@@ -171,14 +181,14 @@ void fp4_tile_kernel(const Fp4Args g) {
       for (int q = 1; q < kXcds; ++q) {  // the shares that end inside this expert
         const int at = (int)((int64_t)ctotal * q / kXcds);
         if (at >= cbase && at < cbase + c)
-          s_share[q] = base * ntn + (int)((int64_t)(at - cbase) * (tiles * ntn) / c);
+          s_share[q] = base * per_tile + (int)((int64_t)(at - cbase) * (tiles * per_tile) / c);
       }
       base += tiles;
       cbase += c;
     }
     if (tid == NT - 1) {
       s_start[g.E] = total;
-      s_share[kXcds] = total * ntn;
+      s_share[kXcds] = total * per_tile;
     }
     __syncthreads();
     first = __builtin_amdgcn_readfirstlane(s_share[xcd]);
@@ -197,26 +207,29 @@ void fp4_tile_kernel(const Fp4Args g) {
     } else {
       auto start = [&](int e) MOE_INLINE { return __builtin_amdgcn_readfirstlane(s_start[e]); };
       int lo = 0, hi = g.E;
-      const int q = item / ntn;
+      const int q = item / per_tile;
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (start(mid) <= q) lo = mid; else hi = mid;
       }
       t.e = lo;
       tiles = start(lo + 1) - start(lo);
-      local = item - ntn * start(lo);
+      local = item - per_tile * start(lo);
       fp4_segment(g, t.e, beg, end);
     }
     constexpr int kGroup = 8;
-    const int group = local / (kGroup * ntn) * kGroup;
-    local -= group * ntn;
+    const int group = local / (kGroup * per_tile) * kGroup;
+    local -= group * per_tile;
     const int in_group = min(kGroup, tiles - group), nt = local / in_group;
     const int mt = group + local - nt * in_group;
+    t.part = __builtin_amdgcn_readfirstlane(nt / ntn);
+    t.s0 = nst * t.part / g.split;
+    t.s1 = nst * (t.part + 1) / g.split;
     // tiles of even height, in steps of a fragment per wavefront row
     const int height = div_up(div_up(end - beg, tiles), 32 * WM) * 32 * WM;
     t.m0 = __builtin_amdgcn_readfirstlane(beg + mt * height);
     t.rows = __builtin_amdgcn_readfirstlane(min(height, end - t.m0));
-    t.n0 = __builtin_amdgcn_readfirstlane(nt * cols);
+    t.n0 = __builtin_amdgcn_readfirstlane((nt - t.part * ntn) * cols);
     t.e = __builtin_amdgcn_readfirstlane(t.e);
     return t;
   };
@@ -228,13 +241,15 @@ void fp4_tile_kernel(const Fp4Args g) {
   const uint8_t* a_ptr[GATHER ? BM / kRpl : 1];
   uint32_t a_off = 0, a_last = 0, b_off = 0, b_last[2] = {0, 0};
   const uint8_t* sc_ptr;  // this thread's row of scales
-  u32x2 sc;               // its bytes of the stage copied last
+  // Its words: 0, 1 of the stage whose scales are to be stored next, 2, 3 of the one after it where
+  // two were loaded at once
+  u32x4 sc;
   const int pos = tid % 8, piece = pos ^ rows_swizzle(tid / 8);
   const uint32_t b_stride = (gated ? 32 : 64) * b_ld;  // from a wavefront column's rows to the next's
   // the row of scales this thread brings: of A, then of B (a thread behind them one again)
   const int sc_row = tid < BM + BN ? tid : tid - (BM + BN);
   const bool scales_a = __builtin_amdgcn_readfirstlane(sc_row) < BM;  // whole wavefronts
-  uint32_t sc_at[2];  // the LDS places of its two words
+  uint32_t sc_at[2];  // the LDS places of its two words of a stage
   {
     const int t = scales_a ? sc_row : sc_row - BM, r = t & 31, f = t >> 5;
 #pragma unroll
@@ -251,13 +266,13 @@ void fp4_tile_kernel(const Fp4Args g) {
 #pragma unroll
       for (int i = 0; i < BM / kRpl; ++i)
         a_ptr[i] = g.x + (size_t)token_of(t.m0 + min(i * kRpl + tid / 8, t.rows - 1)) * a_ld +
-                   16 * piece;
+                   t.s0 * kAStep + 16 * piece;
     } else {
-      a_base = g.x + (size_t)t.m0 * a_ld;
+      a_base = g.x + (size_t)t.m0 * a_ld + t.s0 * kAStep;
       a_off = (uint32_t)(tid / 8) * a_ld + 16 * piece;
       a_last = (uint32_t)(t.rows - 1) * a_ld + 16 * piece;
     }
-    const size_t w0 = ((size_t)t.e * g.N + t.n0) * b_ld;
+    const size_t w0 = ((size_t)t.e * g.N + t.n0) * b_ld + t.s0 * 128;
     const bool second = gated || t.n0 + 32 < g.N;  // the odd fragments have rows of their own
     b_base[0] = g.w.codes + w0;
     b_base[1] = gated ? g.up.codes + w0 : g.w.codes + w0 + (second ? 32 * b_ld : 0);
@@ -291,7 +306,7 @@ void fp4_tile_kernel(const Fp4Args g) {
       const uint8_t* base;
       uint32_t off;
       b_src(i - kA, base, off);
-      copy_to_lds(base, off, la + kABytes + (i - kA) * NT * 16);
+      copy_to_lds<ONCE>(base, off, la + kABytes + (i - kA) * NT * 16);
     } else {
       const int r = i % (BM / kRpl), sub = i / (BM / kRpl);
       if constexpr (GATHER)
@@ -339,35 +354,46 @@ void fp4_tile_kernel(const Fp4Args g) {
     for (int h = 0; h < 2; ++h)
       *(MOE_LDS uint32_t*)(uintptr_t)(lds0 + slot * kSlot + sc_at[h]) = sc[h];
   };
+  // Whether load i brings rows that nm fragments use (of B: always).
+  auto needed = [](int i, int nm) MOE_INLINE {
+    return i >= kA || i % (BM / kRpl) * kRpl < 32 * WM * nm;
+  };
 
   // The copies run ahead of the arithmetic through this block's items in order: the item being
   // copied, its next stage, its fragment rows.
-  int cp_idx = first, cp_stage = 0;
+  int cp_idx = first, cp_stage = 0, cp_end = 0, cp_nm = FM;
   auto begin_copies = [&]() MOE_INLINE {
     int tid_v = tid;  // through an empty statement, see the epilogue
     asm volatile("" : "+v"(tid_v));
-    setup(find(cp_idx), tid_v);
-    cp_stage = 0;
+    const Item t = find(cp_idx);
+    setup(t, tid_v);
+    cp_stage = t.s0;
+    cp_end = t.s1;
+    cp_nm = div_up(t.rows, 32 * WM);
   };
   auto copies_done = [&]() MOE_INLINE {  // a stage was copied
     ++cp_stage;
     next_stage();  // (a branch here would split the stage loop's block)
   };
   auto copies_next = [&]() MOE_INLINE {  // on to the next item where all stages are copied
-    if (cp_stage < nst || cp_idx >= last) return;
+    if (cp_stage < cp_end || cp_idx >= last) return;
     cp_idx += slots;
     if (cp_idx < last) begin_copies();
   };
   auto copy_any = [&](int slot) MOE_INLINE {
     const uint32_t la = slot_lds(slot);
     const int left = nb - cp_stage * kStageBlocks;
-    sc = scale_words(sc_ptr, cp_stage * kStageBlocks, nb);
+    const u32x2 v = scale_words(sc_ptr, cp_stage * kStageBlocks, nb);
+    sc[0] = v[0];
+    sc[1] = v[1];
     if (left >= kStageBlocks) {
 #pragma unroll
-      for (int i = 0; i < kA + kB; ++i) copy_piece(la, i);
+      for (int i = 0; i < kA + kB; ++i)
+        if (needed(i, cp_nm)) copy_piece(la, i);
     } else {
 #pragma unroll
-      for (int i = 0; i < kA + kB; ++i) copy_piece_tail(la, i, left);
+      for (int i = 0; i < kA + kB; ++i)
+        if (needed(i, cp_nm)) copy_piece_tail(la, i, left);
     }
   };
 
@@ -418,25 +444,28 @@ void fp4_tile_kernel(const Fp4Args g) {
     sb[0] = nb_[0];
     sb[1] = nb_[1];
   };
+  enum { kNone, kCopy, kCopyScales };  // what step 3 copies: a stage, with the scales of two
   // Step S of a stage from `cur`; the fragments of the step after it are read meanwhile (of the
-  // next stage behind step 3, with its scales), and with COPY the copies of a whole stage are
+  // next stage behind step 3, with its scales), and with kCopy the copies of a whole stage are
   // issued into the slot that this stage no longer reads.
   auto step = [&](auto s_c, int slot, auto nm_c, auto copy_c) MOE_INLINE {
     constexpr int S = decltype(s_c)::value, NM = decltype(nm_c)::value;
     Frags& cur = S % 2 ? f1 : f0;
     Frags& nxt = S % 2 ? f0 : f1;
-    constexpr bool COPY = decltype(copy_c)::value;
+    constexpr bool COPY = decltype(copy_c)::value != kNone;
     constexpr int kNext = (S + 1) % 4;
     const uint32_t so = (S == 3 ? slot ^ 1 : slot) * kSlot;
     const uint32_t la = COPY ? slot_lds(slot) : 0;
-    if constexpr (COPY) __builtin_memcpy(&sc, sc_ptr + cp_stage * kStageBlocks, 8);
+    if constexpr (decltype(copy_c)::value == kCopyScales)
+      __builtin_memcpy(&sc, sc_ptr + cp_stage * kStageBlocks, 16);
     if constexpr (S == 3) read_scales(so);
 #pragma unroll
     for (int m = 0; m < NM; ++m) {
       if constexpr (COPY) {
         constexpr int per = (kA + kB + NM - 1) / NM;
 #pragma unroll
-        for (int q = m * per; q < (m + 1) * per && q < kA + kB; ++q) copy_piece(la, q);
+        for (int q = m * per; q < (m + 1) * per && q < kA + kB; ++q)
+          if (needed(q, NM)) copy_piece(la, q);
       }
       if (m == 0) {
         read_b(nxt, so, kNext, 0);
@@ -451,57 +480,62 @@ void fp4_tile_kernel(const Fp4Args g) {
   };
 
   // ---- epilogue: element 4 q + i of lane l is column 8 q + 4 h + i of row l % 32 of a fragment
-  // pair; after the exchange between the half wavefronts a lane holds 8 consecutive columns.
-  auto epilogue = [&](const Item& t, int nm) MOE_INLINE {
+  // pair; after the exchange between the half wavefronts a lane holds 8 consecutive columns.  One
+  // copy per activation (a choice per element was 8 us of a 256 x 256 tile's 10).
+  auto epilogue_of = [&](const Item& t, int nm, auto act_c) MOE_INLINE {
+    constexpr int ACT = decltype(act_c)::value;
     // through an empty statement: otherwise what derives from the lane below is computed before
     // the items' loop and kept in registers through it
     int lane = threadIdx.x & 63;
     asm volatile("" : "+v"(lane));
     const int r32 = lane & 31, h = lane >> 5;
-    const int nf = gated ? 1 : 2;
-#pragma unroll
-    for (int f = 0; f < 2; ++f) {
-      if (f >= nf) break;
-      const int cf = t.n0 + (gated ? wn * 32 : wn * 64 + 32 * f);
-      if (cf >= g.N) break;
-      float bias[16], ub[16];
+    auto biases = [&](const void* bias, int cf, float* v) MOE_INLINE {
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const int c = cf + 8 * q + 4 * h;
-        uint2 v = make_uint2(0, 0), u = make_uint2(0, 0);
-        if (g.w.bias && c < g.N) v = *(const uint2*)((const uint16_t*)g.w.bias + (size_t)t.e * g.N + c);
-        if (g.up.bias && c < g.N) u = *(const uint2*)((const uint16_t*)g.up.bias + (size_t)t.e * g.N + c);
-        bias[4 * q] = bf16_lo(v.x); bias[4 * q + 1] = bf16_hi(v.x);
-        bias[4 * q + 2] = bf16_lo(v.y); bias[4 * q + 3] = bf16_hi(v.y);
-        ub[4 * q] = bf16_lo(u.x); ub[4 * q + 1] = bf16_hi(u.x);
-        ub[4 * q + 2] = bf16_lo(u.y); ub[4 * q + 3] = bf16_hi(u.y);
+        uint2 b = make_uint2(0, 0);
+        if (bias && c < g.N) b = *(const uint2*)((const uint16_t*)bias + (size_t)t.e * g.N + c);
+        v[4 * q] = bf16_lo(b.x);
+        v[4 * q + 1] = bf16_hi(b.x);
+        v[4 * q + 2] = bf16_lo(b.y);
+        v[4 * q + 3] = bf16_hi(b.y);
       }
+    };
+    // 32 columns from cf on: act(z + b), times the factors of a second fragment if there are any
+    auto columns = [&](int f, int cf, auto gated_c) MOE_INLINE {
+      constexpr bool GATED = decltype(gated_c)::value;
+      float b[16], ub[16];
+      biases(g.w.bias, cf, b);
+      if constexpr (GATED) biases(g.up.bias, cf, ub);
 #pragma unroll
       for (int m = 0; m < FM; ++m) {
         if (m >= nm) break;
         const int r = (m * WM + wm) * 32 + r32;
         const size_t row = (size_t)(t.m0 + r) * g.N;
         const bool in = r < t.rows;
-        bool named = true;
+        bool named = true;  // (a row whose token lies outside x: zeros)
         if constexpr (GATHER)
           named = (unsigned)g.row_token[t.m0 + min(r, t.rows - 1)] < (unsigned)g.T;
 #pragma unroll
         for (int p = 0; p < 2; ++p) {  // 16 columns: 8 of a lane's own and of its partner's
           const int c = cf + 16 * p + 8 * h;
           const bool live = in && c < g.N;
-          uint4 res = make_uint4(0, 0, 0, 0);
-          if (g.residual && live) res = *(const uint4*)(g.residual + row + c);
-          swap32(res.x, res.z);
-          swap32(res.y, res.w);
-          float rf[8], y[8];
-          unpack8(res, rf);
+          float y[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const int k = 8 * p + i;
-            float z = named ? acc[m][f][k] : 0.0f;
-            y[i] = act_value(g.act, z + bias[k]);
-            if (gated) y[i] *= (named ? acc[m][1][k] : 0.0f) + ub[k];
-            y[i] += rf[i];
+            y[i] = act_value(ACT, (named ? acc[m][f][k] : 0.0f) + b[k]);
+            if constexpr (GATED) y[i] *= (named ? acc[m][1][k] : 0.0f) + ub[k];
+          }
+          if (g.residual) {  // uniform
+            uint4 res = make_uint4(0, 0, 0, 0);
+            if (live) res = *(const uint4*)(g.residual + row + c);
+            swap32(res.x, res.z);
+            swap32(res.y, res.w);
+            float rf[8];
+            unpack8(res, rf);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y[i] += rf[i];
           }
           uint4 o = pack8(y);
           swap32(o.x, o.z);
@@ -509,6 +543,48 @@ void fp4_tile_kernel(const Fp4Args g) {
           if (live) *(uint4*)(g.y + row + c) = o;
         }
       }
+    };
+    if (gated) {
+      const int cf = t.n0 + wn * 32;
+      if (cf < g.N) columns(0, cf, std::true_type{});
+    } else {
+      const int cf = t.n0 + wn * 64;
+      if (cf < g.N) columns(0, cf, std::false_type{});
+      if (cf + 32 < g.N) columns(1, cf + 32, std::false_type{});
+    }
+  };
+  auto epilogue = [&](const Item& t, int nm) MOE_INLINE {
+    if (g.split > 1) {  // the sums, for the joining kernel
+      int lane = threadIdx.x & 63;
+      asm volatile("" : "+v"(lane));
+      const size_t width = gated ? 2 * (size_t)g.N : g.N;
+#pragma unroll
+      for (int f = 0; f < 2; ++f) {
+        const int c0 = t.n0 + (gated ? wn * 32 : wn * 64 + 32 * f) + 4 * (lane >> 5);
+        float* const col = g.part + (size_t)t.part * g.R * width + (gated && f ? g.N : 0);
+#pragma unroll
+        for (int m = 0; m < FM; ++m) {
+          if (m >= nm) break;
+          const int r = (m * WM + wm) * 32 + (lane & 31);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int c = c0 + 8 * q;
+            const f32x4_t v = {acc[m][f][4 * q], acc[m][f][4 * q + 1], acc[m][f][4 * q + 2],
+                               acc[m][f][4 * q + 3]};
+            if (r < t.rows && c < g.N) *(f32x4_t*)(col + (t.m0 + r) * width + c) = v;
+          }
+        }
+      }
+      return;
+    }
+    switch (g.act) {
+      case MOE_ACT_RELU: epilogue_of(t, nm, std::integral_constant<int, MOE_ACT_RELU>{}); break;
+      case MOE_ACT_RELU2: epilogue_of(t, nm, std::integral_constant<int, MOE_ACT_RELU2>{}); break;
+      case MOE_ACT_SILU: epilogue_of(t, nm, std::integral_constant<int, MOE_ACT_SILU>{}); break;
+      case MOE_ACT_GELU_TANH:
+        epilogue_of(t, nm, std::integral_constant<int, MOE_ACT_GELU_TANH>{});
+        break;
+      default: epilogue_of(t, nm, std::integral_constant<int, MOE_ACT_NONE>{});
     }
   };
 
@@ -528,8 +604,7 @@ void fp4_tile_kernel(const Fp4Args g) {
   wait_copies();
   block_barrier();
   int slot = 0;
-  using Yes = std::true_type;
-  using No = std::false_type;
+  using No = std::integral_constant<int, kNone>;
   constexpr auto S0 = std::integral_constant<int, 0>{};
   constexpr auto S1 = std::integral_constant<int, 1>{};
   constexpr auto S2 = std::integral_constant<int, 2>{};
@@ -546,25 +621,36 @@ void fp4_tile_kernel(const Fp4Args g) {
       for (int n = 0; n < 2; ++n) read_b(f0, slot * kSlot, 0, n);
 #pragma unroll
       for (int m = 0; m < NM; ++m) read_a(f0, slot * kSlot, 0, m);
-      // Stages behind whose barrier a whole stage of this same item is copied: without branches.
-      const int whole = nb / kStageBlocks;
-      const int fast = cp_idx == idx ? max(whole - cp_stage, 0) : 0;
+      // Stages behind whose barrier a whole stage of this same item is copied, without branches and
+      // by two: 16 bytes of a row's scales at a time (by one, a quarter of the traffic out of the
+      // L2 was lines of scales of which 8 bytes were used).
+      const int whole = min(nb / kStageBlocks, cp_end);
+      const int fast = cp_idx == idx ? max(whole - cp_stage, 0) / 2 * 2 : 0;
+      const int stages = item.s1 - item.s0;
       int s = 0;
-      for (; s < fast; ++s) {
+      auto stage = [&](auto copy_c) MOE_INLINE {
         step(S0, slot, nm_c, No{});
         step(S1, slot, nm_c, No{});
         step(S2, slot, nm_c, No{});
         wait_copies();
         store_scales(slot ^ 1);
+        if constexpr (decltype(copy_c)::value == kCopy) {  // the second of two
+          sc[0] = sc[2];
+          sc[1] = sc[3];
+        }
         wait_copies();
         block_barrier();
-        step(S3, slot, nm_c, Yes{});
+        step(S3, slot, nm_c, copy_c);
         use_scales();
         copies_done();
         slot ^= 1;
+      };
+      for (; s < fast; s += 2) {
+        stage(std::integral_constant<int, kCopyScales>{});
+        stage(std::integral_constant<int, kCopy>{});
       }
       // The others: a partial stage, the next item's first ones, or nothing left to copy.
-      for (; s < nst; ++s) {
+      for (; s < stages; ++s) {
         copies_next();
         step(S0, slot, nm_c, No{});
         step(S1, slot, nm_c, No{});
@@ -613,15 +699,67 @@ int cu_count() {
   return n;
 }
 
-enum Fp4Kernel { kStream = 0, kTile256, kTile128 };
+enum Fp4Kernel { kStream = 0, kTile256, kTile128, kTile128Once };
 
-Fp4Kernel fp4_plan(const moe_grouped& p, bool eight, bool gated) {
-  const int64_t rows = p.R / p.E;
-  (void)eight;
-  (void)gated;
-  if (rows > 192) return kTile256;
-  if (rows > 32) return kTile128;
-  return kStream;
+// Which kernel a call takes and into how many parts it cuts the reduction, from its sizes alone
+// (the row counts are on the device).  Heights are those for x in 4 bits; for 8 they are half.
+struct Fp4Plan {
+  Fp4Kernel kernel;
+  int split;
+};
+Fp4Plan fp4_plan(const moe_grouped& p, bool eight, bool gated) {
+  const int64_t rows = p.R / p.E, active = std::min(p.E, std::max(p.R, 1));
+  const int stages = div_up(p.K, 256), big = eight ? 128 : 256;
+  // tiles, with half of the experts having one more than their rows need
+  auto tiles = [&](int bm, int bn) {
+    const int64_t mt = std::max<int64_t>(active, p.R / bm + (p.E > 1 ? p.E / 2 : 1));
+    return mt * div_up(p.N, gated ? bn / 2 : bn);
+  };
+  const int64_t n256 = tiles(big, 256), n128 = tiles(big / 2, 128);
+  // few rows, and few tiles or short reductions: latency.  (16 rows for each of 128 experts, 2048 ->
+  // 768 twice: 55 us, tiles 59; 8 for each of 64, 4096 -> 1408 twice: 91 and 79 us.  x in 8 bits: 1 for
+  // each of the 128: 40 and 33 us; 4 of one 7168 -> 4096: 15 us, tiles in 4 parts the same, 16 of
+  // it 18 and 15.)
+  if (rows <= (eight ? 4 : 16) && (n128 < 256 || (!eight && stages <= 8))) return {kStream, 1};
+  // (4 bits: 128 rows for each of 64 experts, 4096 -> 1408: 77 us, with 128-tiles 80; 96 rows: 69 and
+  // 62, with the non-temporal hint 58.  8 bits: 64 rows 108 and 123 us; 48 rows 97 and 100, with the
+  // hint 97.  One 4096 x 2048 x 2048, 128 tiles: 23 and 19 us; 4096 x 7168 x 4096, 256 tiles: 67
+  // and 80 us.)
+  if (16 * rows > 7 * big && n256 >= 192) return {kTile256, 1};
+  // the weights are read once: with the non-temporal hint (8 rows for each of 256 experts, 7168 -> 1024
+  // twice: 388 and 358 us)
+  if (n128 >= 256) return {8 * rows <= 3 * big ? kTile128Once : kTile128, 1};
+  // few tiles: long reductions in parts (128 x 7168 x 4096, 32 tiles: 26 us, in 4 parts 18; 512 rows,
+  // 128 tiles: 26.3, in 2 parts 25.6, in 4 28; 1024 x 2048 x 2048: 12, in 2 parts 18)
+  return {kTile128, (int)std::max<int64_t>(1, std::min<int64_t>(stages / 7, 256 / n128))};
+}
+
+// Adds the parts of a split reduction in order and finishes: 4 columns per thread.
+__global__ __launch_bounds__(256) void fp4_join_kernel(const Fp4Args g) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int nq = g.N / 4, r = (int)(i / nq), c = (int)(i % nq) * 4;
+  int lo, hi;
+  fp4_segment(g, 0, lo, hi);
+  if (g.offsets) hi = min(max(g.offsets[g.E], 0), g.R);
+  if (r < lo || r >= hi) return;  // (rows outside every expert are left alone)
+  const bool gated = g.up.codes != nullptr;
+  const size_t width = gated ? 2 * (size_t)g.N : g.N, o = r * width + c;
+  f32x4_t z = {}, u = {};
+  for (int p = 0; p < g.split; ++p) {
+    const float* const part = g.part + (size_t)p * g.R * width + o;
+    z += *(const f32x4_t*)part;
+    if (gated) u += *(const f32x4_t*)(part + g.N);
+  }
+  int e = 0;
+  if ((g.w.bias || g.up.bias) && g.offsets) {  // the expert of row r
+    int top = g.E;
+    while (top - e > 1) {
+      const int mid = (e + top) >> 1;
+      if (g.offsets[mid] <= r) e = mid; else top = mid;
+    }
+  }
+  if (g.row_token && (unsigned)g.row_token[r] >= (unsigned)g.T) z = u = f32x4_t{};
+  fp4_finish4(g, e, r, c, z, u);
 }
 
 template <bool EIGHT, bool GATHER>
@@ -629,29 +767,44 @@ void launch_tiles(const Fp4Args& g, Fp4Kernel kernel, hipStream_t s) {
   if (kernel == kTile256)
     hipLaunchKernelGGL((fp4_tile_kernel<EIGHT, GATHER, EIGHT ? 128 : 256, 2, 4>), dim3(cu_count()),
                        dim3(512), 0, s, g);
-  else
+  else if (kernel == kTile128)
     hipLaunchKernelGGL((fp4_tile_kernel<EIGHT, GATHER, EIGHT ? 64 : 128, 2, 2>),
+                       dim3(2 * cu_count()), dim3(256), 0, s, g);
+  else
+    hipLaunchKernelGGL((fp4_tile_kernel<EIGHT, GATHER, EIGHT ? 64 : 128, 2, 2, true>),
                        dim3(2 * cu_count()), dim3(256), 0, s, g);
 }
 
 }  // namespace
 
-size_t grouped_fp4_ws_bytes(const moe_grouped&) { return 0; }
+// (for either type of x, with or without a second weight set)
+size_t grouped_fp4_ws_bytes(const moe_grouped& p) {
+  size_t n = 0;
+  for (int v = 0; v < 4; ++v) {
+    const int split = fp4_plan(p, v & 1, v >> 1).split;
+    if (split > 1) n = std::max(n, align256((size_t)split * p.R * p.N * (v >> 1 ? 8 : 4)));
+  }
+  return n;
+}
 
 hipError_t launch_grouped_fp4(const moe_grouped& p, bool eight, const uint8_t* x_codes,
                               const uint8_t* x_scales, const int32_t* row_token,
                               const int32_t* offsets, const Fp4Weights& w, const Fp4Weights& up,
                               int act, const void* residual, void* y, void* ws, hipStream_t s) {
+  const Fp4Plan plan = fp4_plan(p, eight, up.codes != nullptr);
   const Fp4Args g{x_codes, x_scales, row_token, offsets, w, up, (const uint16_t*)residual,
-                  (uint16_t*)y, p.R, p.T, p.K, p.N, p.E, act, 1, (float*)ws};
-  const Fp4Kernel kernel = fp4_plan(p, eight, up.codes != nullptr);
-  if (kernel == kStream) return launch_fp4_stream(g, eight, s);
+                  (uint16_t*)y, p.R, p.T, p.K, p.N, p.E, act, plan.split, (float*)ws};
+  if (plan.kernel == kStream) return launch_fp4_stream(g, eight, s);
   if (eight) {
-    if (row_token) launch_tiles<true, true>(g, kernel, s);
-    else launch_tiles<true, false>(g, kernel, s);
+    if (row_token) launch_tiles<true, true>(g, plan.kernel, s);
+    else launch_tiles<true, false>(g, plan.kernel, s);
   } else {
-    if (row_token) launch_tiles<false, true>(g, kernel, s);
-    else launch_tiles<false, false>(g, kernel, s);
+    if (row_token) launch_tiles<false, true>(g, plan.kernel, s);
+    else launch_tiles<false, false>(g, plan.kernel, s);
+  }
+  if (plan.split > 1) {
+    const int64_t n = (int64_t)g.R * (g.N / 4);
+    hipLaunchKernelGGL(fp4_join_kernel, dim3((unsigned)div_up64(n, 256)), dim3(256), 0, s, g);
   }
   return hipGetLastError();
 }

@@ -49,40 +49,76 @@ __global__ __launch_bounds__(64 * kParts) void fp4_stream_kernel(const Fp4Args g
     const uint8_t* xp = g.x + row * x_ld;
     const uint8_t* xs = g.xs + (size_t)row * nb;
     f32x16_t acc[2] = {};
-    for (int s = s0; s < s1; ++s) {
-      const u32x4 zero = {0, 0, 0, 0};
+    struct Stage {
       u32x4 w[2][4], x[4][2];
+      uint32_t sw[2], sx;
+    };
+    auto load = [&](Stage& t, int s, auto whole_c) {  // whole: all of its blocks are there
+      constexpr bool WHOLE = decltype(whole_c)::value;
+      const u32x4 zero = {0, 0, 0, 0};
       const int b0 = 8 * s + 4 * h;  // this lane's first block
 #pragma unroll
       for (int f = 0; f < 2; ++f)
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-          w[f][q] = b0 + q < nb ? *(const u32x4*)(wp[f] + (size_t)(b0 + q) * 16) : zero;
+          t.w[f][q] = WHOLE || b0 + q < nb
+                          ? *(const u32x4*)(wp[f] + (size_t)(b0 + q) * 16)
+                          : zero;
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         if constexpr (EIGHT) {
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const int b = 8 * s + 4 * i + q;
-            x[q][i] = b < nb ? *(const u32x4*)(xp + (size_t)b * 32 + 16 * h) : zero;
+            t.x[q][i] = WHOLE || b < nb ? *(const u32x4*)(xp + (size_t)b * 32 + 16 * h) : zero;
           }
         } else {
-          x[q][0] = b0 + q < nb ? *(const u32x4*)(xp + (size_t)(b0 + q) * 16) : zero;
+          t.x[q][0] = WHOLE || b0 + q < nb ? *(const u32x4*)(xp + (size_t)(b0 + q) * 16) : zero;
         }
       }
-      const uint32_t sw[2] = {scale_word(ws[0], b0, nb), scale_word(ws[1], b0, nb)};
-      const uint32_t sx = scale_word(xs, b0, nb);
+      if constexpr (WHOLE) {
+        __builtin_memcpy(&t.sw[0], ws[0] + b0, 4);
+        __builtin_memcpy(&t.sw[1], ws[1] + b0, 4);
+        __builtin_memcpy(&t.sx, xs + b0, 4);
+      } else {
+        t.sw[0] = scale_word(ws[0], b0, nb);
+        t.sw[1] = scale_word(ws[1], b0, nb);
+        t.sx = scale_word(xs, b0, nb);
+      }
+    };
+    auto multiply = [&](const Stage& t) {
+      i32x8_t x[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) x[q] = EIGHT ? operand8(t.x[q][0], t.x[q][1]) : operand4(t.x[q][0]);
 #pragma unroll
       for (int f = 0; f < 2; ++f) {
-        const i32x8_t x0 = EIGHT ? operand8(x[0][0], x[0][1]) : operand4(x[0][0]);
-        const i32x8_t x1 = EIGHT ? operand8(x[1][0], x[1][1]) : operand4(x[1][0]);
-        const i32x8_t x2 = EIGHT ? operand8(x[2][0], x[2][1]) : operand4(x[2][0]);
-        const i32x8_t x3 = EIGHT ? operand8(x[3][0], x[3][1]) : operand4(x[3][0]);
-        acc[f] = fp4_product<EIGHT, 0>(operand4(w[f][0]), x0, acc[f], sw[f], sx);
-        acc[f] = fp4_product<EIGHT, 1>(operand4(w[f][1]), x1, acc[f], sw[f], sx);
-        acc[f] = fp4_product<EIGHT, 2>(operand4(w[f][2]), x2, acc[f], sw[f], sx);
-        acc[f] = fp4_product<EIGHT, 3>(operand4(w[f][3]), x3, acc[f], sw[f], sx);
+        acc[f] = fp4_product<EIGHT, 0>(operand4(t.w[f][0]), x[0], acc[f], t.sw[f], t.sx);
+        acc[f] = fp4_product<EIGHT, 1>(operand4(t.w[f][1]), x[1], acc[f], t.sw[f], t.sx);
+        acc[f] = fp4_product<EIGHT, 2>(operand4(t.w[f][2]), x[2], acc[f], t.sw[f], t.sx);
+        acc[f] = fp4_product<EIGHT, 3>(operand4(t.w[f][3]), x[3], acc[f], t.sw[f], t.sx);
       }
+    };
+    using Yes = std::true_type;
+    using No = std::false_type;
+    const int whole = min(s1, nb / 8);
+    int s = s0;
+    for (; s + 2 <= whole; s += 2) {  // two at a time: their loads are in flight together
+      Stage a, b;
+      load(a, s, Yes{});
+      load(b, s + 1, Yes{});
+      __builtin_amdgcn_sched_barrier(0);
+      multiply(a);
+      multiply(b);
+    }
+    for (; s < whole; ++s) {
+      Stage a;
+      load(a, s, Yes{});
+      multiply(a);
+    }
+    if (s < s1) {  // the last, partial stage
+      Stage a;
+      load(a, s, No{});
+      multiply(a);
     }
     // element 4 q + i of lane l: column 8 q + 4 h + i of row l % 32
 #pragma unroll
