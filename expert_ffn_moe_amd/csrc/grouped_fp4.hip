@@ -710,9 +710,9 @@ struct Fp4Plan {
 Fp4Plan fp4_plan(const moe_grouped& p, bool eight, bool gated) {
   const int64_t rows = p.R / p.E, active = std::min(p.E, std::max(p.R, 1));
   const int stages = div_up(p.K, 256), big = eight ? 128 : 256;
-  // tiles, with half of the experts having one more than their rows need
+  // tiles, with half of the experts that have rows having one more than those need
   auto tiles = [&](int bm, int bn) {
-    const int64_t mt = std::max<int64_t>(active, p.R / bm + (p.E > 1 ? p.E / 2 : 1));
+    const int64_t mt = std::max<int64_t>(active, p.R / bm + (p.E > 1 ? active / 2 : 1));
     return mt * div_up(p.N, gated ? bn / 2 : bn);
   };
   const int64_t n256 = tiles(big, 256), n128 = tiles(big / 2, 128);

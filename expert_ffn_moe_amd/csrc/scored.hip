@@ -618,7 +618,9 @@ __global__ __launch_bounds__(256) void scored_bwd_kernel(const ScoredBwdArgs a) 
         word x;
 #pragma unroll
         for (int j = 0; j < W; ++j) x[j] = v[i + j];
-        if (lane * EPL + i < a.E) *(word*)(a.dl + row + lane * EPL + i) = x;
+        // (written once: 16384 x 256 in 9.2 us with the hint, 10.7 without)
+        if (lane * EPL + i < a.E)
+          __builtin_nontemporal_store(x, (word*)(a.dl + row + lane * EPL + i));
       }
     } else {
 #pragma unroll
@@ -628,7 +630,9 @@ __global__ __launch_bounds__(256) void scored_bwd_kernel(const ScoredBwdArgs a) 
   }
 }
 
-// Tokens per wavefront: several share the pass over their slots where enough wavefronts remain.
+// Tokens per wavefront of the gradient: several share the pass over their slots where enough
+// wavefronts remain (16384 tokens: 10.7 us with 4, 12.7 with 1, 12.4 with 8; 4096: 6.1 with 1, 7.6
+// with 2).
 int tokens_per_wave(const moe_problem& p) {
   int n = 4;
   while (n > 1 && (n * p.k > 64 || p.T / n < 4096)) n /= 2;

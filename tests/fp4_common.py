@@ -46,12 +46,20 @@ def codes8(g, rows, K, narrow):
     return c, s
 
 
+def shifted(t):
+    """A copy of a byte tensor that begins one byte behind an aligned place."""
+    flat = torch.empty(t.numel() + 1, dtype=torch.uint8, device=t.device)
+    out = flat[1:].view(t.shape)
+    out.copy_(t)
+    return out
+
+
 class Case:
     """A product with its inputs; rows that no expert owns have NaN scales and a patterned y, as
     have the tokens that no row names."""
 
     def __init__(self, counts, K, N, x="fp4", act="none", gated=False, bias=False, residual=False,
-                 gather=False, behind=0, front=0, T=None, seed=1, wild=False):
+                 gather=False, behind=0, front=0, T=None, seed=1, wild=False, shift=False):
         self.m = m = moe()
         g = gen(seed)
         E, live = len(counts), sum(counts)
@@ -75,6 +83,8 @@ class Case:
             self.xq = codes8(g, (rows,), K, not self.wide)
         else:
             self.xq = codes4(g, (rows,), K)
+        if shift:  # scales need no alignment
+            self.xq = self.xq[0], shifted(self.xq[1])
         if gather:
             named = torch.zeros(rows, dtype=torch.bool, device=DEV)
             t = self.row_token[front:front + live].long()
@@ -85,6 +95,8 @@ class Case:
             self.xq[1][front + live:] = 255
         self.w = codes4(g, (E, N), K, 3)
         self.up = codes4(g, (E, N), K, 3) if gated else None
+        if shift:
+            self.w = self.w[0], shifted(self.w[1])
         if gated or act != "none":  # pre-activations of a few units: scales down by a power of two
             down = max(0, (K * (2 if not self.eight else 40)).bit_length() // 2)
             for q in (self.w, self.up) if gated else (self.w,):
@@ -111,17 +123,31 @@ class Case:
         return y
 
     def product(self, q, bias):
-        """(z, bound of its error)"""
-        x = (fp4.dequantize8 if self.eight else fp4.dequantize)(*self.xq)
-        x = torch.nan_to_num(x)  # the rows that are not read
-        w = fp4.dequantize(*q)
-        z, size = fp4.linear(x, w, self.segs, bias, self.row_token)
-        tol = sum_tol(self.K, size)
-        if self.wide:  # each of a block's 32 products loses what is 2^-13 of the largest
-            top = lambda v: v.abs().reshape(*v.shape[:-1], -1, 32).amax(-1)  # noqa: E731
-            d, _ = fp4.linear(top(x), top(w), self.segs, None, self.row_token)
-            tol = tol + 32 * 2.0 ** -13 * d
-        return z, tol
+        """(z, bound of its error) of the live rows, expert by expert"""
+        x_of = fp4.dequantize8 if self.eight else fp4.dequantize
+        zs, tols = [torch.zeros(0, self.N, dtype=F64, device=DEV)], []
+        tols.append(zs[0])
+        for e, (lo, hi) in enumerate(self.segs):
+            if lo >= hi:
+                continue
+            rows, dead = slice(lo, hi), None
+            if self.row_token is not None:
+                t = self.row_token[lo:hi].long()
+                dead = (t < 0) | (t >= self.xq[0].shape[0])
+                rows = torch.where(dead, torch.zeros_like(t), t)
+            x, w = x_of(self.xq[0][rows], self.xq[1][rows]), fp4.dequantize(q[0][e], q[1][e])
+            if dead is not None:
+                x = torch.where(dead[:, None], torch.zeros_like(x), x)
+            z, size = x @ w.t(), x.abs() @ w.abs().t()
+            tol = sum_tol(self.K, size)
+            if self.wide:  # each of a block's 32 products loses what is 2^-13 of the largest
+                top = lambda v: v.abs().reshape(v.shape[0], -1, 32).amax(-1)  # noqa: E731
+                tol = tol + 32 * 2.0 ** -13 * (top(x) @ top(w).t())
+            if bias is not None:
+                z, tol = z + bias[e].to(F64), tol + U24 * (size + bias[e].to(F64).abs())
+            zs.append(z)
+            tols.append(tol)
+        return torch.cat(zs), torch.cat(tols)
 
     def check(self, y):
         z, zt = self.product(self.w, self.bias)

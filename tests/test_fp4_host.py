@@ -6,6 +6,7 @@ import pickle
 
 import pytest
 
+from fp4_paths import PATHS, plan
 from grouped_common import fake, moe
 
 INV, UNS, WS, OK = 1, 2, 3, 0
@@ -94,6 +95,49 @@ def test_workspace_op():
     m = moe()
     assert m.GroupedProblem(R=8, K=40, N=16).workspace_bytes(m.OP_GROUPED_FP4) == 0
     assert m.GroupedProblem(R=8, K=64, N=16).workspace_bytes(4) == 0
+
+
+def problem_of(kw):
+    R = sum(kw["counts"]) + kw.get("front", 0) + kw.get("behind", 0)
+    return R, kw["K"], kw["N"], len(kw["counts"])
+
+
+@pytest.mark.parametrize("i", range(len(PATHS)))
+def test_paths_reach_what_they_name(i):
+    four, eight, kw = PATHS[i]
+    gated = kw.get("gated", False)
+    assert plan(*problem_of(kw), False, gated) == four
+    assert plan(*problem_of(kw), True, gated) == eight
+
+
+@pytest.mark.parametrize("R,K,N,E", [
+    (1, 32, 8, 1), (16, 7168, 4096, 1), (17, 7168, 4096, 1), (64, 7168, 1024, 1),
+    (128, 7168, 4096, 1), (512, 7168, 4096, 1), (1024, 7168, 4096, 1), (4096, 2048, 2048, 1),
+    (100, 1 << 20, 64, 1), (300, 3584, 264, 4), (300, 3552, 264, 4), (4096, 2048, 768, 128),
+    (32768, 2048, 768, 128), (131072, 7168, 2048, 256), (0, 7168, 64, 1)])
+def test_workspace_holds_the_parts(R, K, N, E):
+    m = moe()
+    need = 0
+    for eight in (False, True):
+        for gated in (False, True):
+            split = plan(R, K, N, E, eight, gated)[1]
+            if split > 1:
+                need = max(need, -(-split * R * N * (8 if gated else 4) // 256) * 256)
+    assert m.GroupedProblem(R=R, K=K, N=N, E=E).workspace_bytes(m.OP_GROUPED_FP4) == need
+
+
+def test_workspace_refusals():
+    m = moe()
+    names = ("xc", "xs", "off", "wc", "ws_", "y", "w")
+    p = dict(zip(names, fake(len(names))))
+    ws = p.pop("w")
+    g = m.MoeGrouped(100, 100, 7168, 64, 1)
+    need = m.GroupedProblem(R=100, K=7168, N=64).workspace_bytes(m.OP_GROUPED_FP4)
+    assert need > 0
+    assert call(m, g, p) == WS
+    assert call(m, g, p, ws=ws, wsn=need - 1) == WS
+    assert call(m, g, p, ws=at(ws, 16), wsn=need) == INV
+    assert call(m, g, p, ws=p["y"], wsn=need) == INV
 
 
 def test_scoring_refusals():

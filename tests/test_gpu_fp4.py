@@ -3,7 +3,8 @@ fp64 definitions (oracle/fp4.py); tolerances as in tests/grouped_common.py."""
 import pytest
 import torch
 
-from fp4_common import DEV, PATTERN, Case, gen, moe
+from fp4_common import DEV, PATTERN, Case, codes4, gen, moe
+from fp4_paths import PATHS
 from oracle import fp4
 
 pytestmark = pytest.mark.gpu
@@ -152,6 +153,113 @@ def test_grouped_linear_fp4(c):
     case.check(y)
     again = case.run()
     assert torch.equal(y.view(torch.int16), again.view(torch.int16))  # no order of its own
+
+
+@pytest.mark.parametrize("x", ["fp4", "fp8"])
+@pytest.mark.parametrize("i", range(len(PATHS)))
+def test_every_kernel(i, x):
+    case = Case(**PATHS[i][2], x=x, seed=i + 20)
+    y = case.run()
+    case.check(y)
+    assert torch.equal(y.view(torch.int16), case.run().view(torch.int16))
+
+
+@pytest.mark.parametrize("kw", [dict(counts=[300], K=864, N=136), dict(counts=[3], K=864, N=136),
+                                dict(counts=[300, 0, 80], K=1120, N=264, gather=True, x="fp8")],
+                         ids=str)
+def test_scales_need_no_alignment(kw):
+    case = Case(**kw, shift=True)
+    assert case.w[1].data_ptr() % 2 == 1 and case.xq[1].data_ptr() % 2 == 1
+    case.check(case.run())
+
+
+@pytest.mark.parametrize("counts", [[70, 30], [9, 4]])
+def test_rows_and_weights_behind_4_gb(counts):
+    case = Case(counts, 16384, 72, front=600000)  # 4.9 GB of x
+    assert case.xq[0].numel() > 1 << 32
+    case.check(case.run())
+    del case
+    torch.cuda.empty_cache()
+    case = Case([0] * 1022 + counts, 8224, 1048, act="silu")  # 4.4 GB of weights
+    assert case.w[0].numel() > 1 << 32
+    case.check(case.run())
+
+
+def test_more_values_than_one_launch_takes():
+    m = moe()
+    cols, rows = 8192, (1 << 19) + 40  # 2^32 values and 40 rows more
+    x = torch.zeros(rows, cols, dtype=torch.bfloat16, device=DEV)
+    x[-50:] = torch.randn(50, cols, device=DEV).bfloat16()
+    codes, scales = m.quantize_fp4(x)
+    want = m.quantize_fp4(x[-50:].contiguous())
+    assert torch.equal(codes[-50:], want[0]) and torch.equal(scales[-50:], want[1])
+    x.fill_(1.0)
+    m.dequantize_fp4(codes, scales, out=x)
+    assert torch.equal(x[-50:], m.dequantize_fp4(*want)) and not x[:-50].any()
+
+
+def test_two_calls_at_once_on_two_streams():
+    cases = [Case([90, 0, 37, 130], 5600, 264, x=x, gated=True, act="silu", gather=True, seed=s)
+             for s, x in ((3, "fp4"), (4, "fp8"))]
+    ys = [c.new_y() for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for _ in range(5):
+        for c, y, s in zip(cases, ys, streams):
+            with torch.cuda.stream(s):
+                c.run(y)
+    torch.cuda.synchronize()
+    for c, y in zip(cases, ys):
+        c.check(y)
+
+
+def test_two_graphs_that_share_a_workspace():
+    m = moe()
+    cases = [Case([90, 0, 37, 130], 5600, 264, seed=s, bias=True) for s in (5, 6)]
+    ws = m.grouped_workspace(cases[0].p, m.OP_GROUPED_FP4)
+    assert ws is not None
+    ys = [c.new_y() for c in cases]
+    graphs = []
+    for c, y in zip(cases, ys):
+        c.run(y, ws)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            c.run(y, ws)
+        graphs.append(g)
+    for _ in range(3):
+        for y in ys:
+            y.view(torch.uint8).fill_(PATTERN)
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        for c, y in zip(cases, ys):
+            c.check(y)
+
+
+def test_debug_library_reports_bad_offsets_and_tokens():
+    import ctypes
+    m = moe()
+    c = Case([40, 30, 20], 128, 64, gather=True)
+    d = m.debug_lib()
+    m.debug_status()
+
+    def call():
+        y = c.new_y()
+        w = m.MoeFp4Weights(c.w[0].data_ptr(), c.w[1].data_ptr(), None)
+        ptr = lambda t: ctypes.c_void_p(t.data_ptr())  # noqa: E731
+        st = d.moe_grouped_linear_fp4(c.p._ref, m.MOE_FP4, ptr(c.xq[0]), ptr(c.xq[1]),
+                                      ptr(c.row_token), ptr(c.offsets), ctypes.byref(w), None, 0,
+                                      None, ptr(y), None, 0, m._stream())
+        assert st == m.MOE_OK
+        return y
+
+    c.check(call())
+    assert m.debug_status() == 0
+    c.offsets[3] = 4000
+    c.row_token[5] = -7
+    call()
+    assert m.debug_status() == 12
 
 
 def test_nan_scales_and_codes_poison_their_sums_only():

@@ -40,6 +40,14 @@ CASES = [
     (9, 1024, 32, "sigmoid", 64, 9, "top2", "out", True, 1.0, 0, "normal"),
     (300, 48, 4, "softmax", 1, 1, "max", "normal", True, 1.0, 11, "ties"),
     (300, 48, 4, "sigmoid", 4, 2, "top2", None, False, 2.5, 20, "normal"),
+    (65, 37, 5, "sigmoid", 1, 1, "max", "normal", True, 1.0, 0, "normal"),  # rows of odd length
+    (65, 90, 8, "softmax", 3, 2, "top2", "normal", True, 1.0, 0, "ties"),
+    (33, 250, 8, "sigmoid", 5, 2, "top2", "out", False, 1.0, 0, "masked"),
+    (47, 256, 8, "sigmoid", 1, 1, "max", "same", True, 1.0, 0, "lane"),  # one lane's experts lead
+    (47, 256, 7, "sigmoid", 1, 1, "max", None, True, 1.0, 0, "lane"),
+    (5000, 128, 8, "softmax", 1, 1, "max", "normal", True, 1.0, 0, "close"),
+    (5000, 256, 8, "sigmoid", 8, 4, "top2", "normal", True, 2.5, 0, "close"),
+    (3001, 64, 8, "sigmoid", 8, 4, "max", "close", False, 2.5, 0, "close"),
 ]
 
 
@@ -120,6 +128,68 @@ def test_softmax_without_bias_is_route_grouped():
     b = m.route_scored(p, x, m.Scoring("softmax", 8, 3, "max"))
     assert torch.equal(a[0], b[0])
     assert ((a[1] - b[1]).abs() <= 1e-6 * b[1]).all()
+
+
+def test_logits_that_begin_between_words():
+    m = moe()
+    T, E, k = 40, 64, 4
+    p = m.Problem(T=T, H=64, E=E, k=k, I=64)
+    sc = m.Scoring("sigmoid", 4, 2, "top2")
+    x, b = make_logits(T, E, 3), make_bias(E, 3)
+    want = m.route_scored(p, x.cuda(), sc, bias=b.cuda())
+    flat = torch.empty(T * E + 1, device="cuda")
+    at = flat[1:].view(T, E)
+    at.copy_(x)
+    got = m.route_scored(p, at, sc, bias=b.cuda())
+    assert all(torch.equal(a, q) for a, q in zip(got, want))
+    dw = torch.randn(T, k, device="cuda")
+    dl = torch.empty(T * E + 1, device="cuda")[1:].view(T, E)
+    m.route_scored_backward(p, at, sc, got[0], got[1], dw, out=dl)
+    assert torch.equal(dl, m.route_scored_backward(p, x.cuda(), sc, got[0], got[1], dw))
+
+
+def test_more_than_2_31_logits():
+    m = moe()
+    E, k, n = 256, 8, 300
+    T = (1 << 23) + n
+    x = torch.zeros(T, E, device="cuda")
+    x[-n:] = make_logits(n, E, 4).cuda()
+    b = make_bias(E, 4).cuda()
+    sc = m.Scoring("sigmoid", 8, 4, "top2", 2.5)
+    big, small = (m.Problem(T=t, H=64, E=E, k=k, I=64) for t in (T, n))
+    got = m.route_scored(big, x, sc, bias=b)
+    tail = x[-n:].contiguous()
+    want = m.route_scored(small, tail, sc, bias=b)
+    assert all(torch.equal(a[-n:], q) for a, q in zip(got, want))
+    dw = torch.zeros(T, k, device="cuda")
+    dw[-n:] = torch.randn(n, k, device="cuda")
+    dl = m.route_scored_backward(big, x, sc, got[0], got[1], dw)
+    assert torch.equal(dl[-n:], m.route_scored_backward(small, tail, sc, want[0], want[1],
+                                                        dw[-n:].contiguous()))
+    assert not dl[:-n].any()
+
+
+def test_debug_library_reports_bad_ids():
+    import ctypes
+    m = moe()
+    T, E, k = 70, 16, 2
+    p = m.Problem(T=T, H=64, E=E, k=k, I=64)
+    sc = m.Scoring("sigmoid")
+    x = make_logits(T, E, 2).cuda()
+    ids, w, _ = m.route_scored(p, x, sc)
+    dw, dl = torch.randn(T, k, device="cuda"), torch.empty(T, E, device="cuda")
+    want = m.route_scored_backward(p, x, sc, ids, w, dw)
+    d, c = m.debug_lib(), p.c()
+    m.debug_status()
+    ptr = lambda t: ctypes.c_void_p(t.data_ptr())  # noqa: E731
+    run = lambda: d.moe_route_scored_backward(  # noqa: E731
+        ctypes.byref(c), sc._ref, ptr(x), ptr(ids), ptr(w), ptr(dw), ptr(dl), m._stream())
+    assert run() == m.MOE_OK and m.debug_status() == 0 and torch.equal(dl, want)
+    ids[3, 1], ids[9, 0] = 99, -4
+    assert run() == m.MOE_OK and m.debug_status() & 1
+    keep = torch.ones(T, dtype=torch.bool)
+    keep[[3, 9]] = False
+    assert torch.equal(dl[keep.cuda()], want[keep.cuda()])
 
 
 def test_large_batch_capture_and_streams():
