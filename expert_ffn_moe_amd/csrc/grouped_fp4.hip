@@ -121,6 +121,8 @@ void fp4_tile_kernel(const Fp4Args g) {
   static_assert(BM % kRpl == 0 && BM + BN <= NT && (kRpl == 64 || kRpl == 32), "");
   __shared__ __align__(1024) char smem[2 * kSlot];
   __shared__ int s_start[kMaxE + 1];  // M tiles before each expert
+  __shared__ int s_beg[kMaxE + 1];    // its first row (read from memory for every item: 32.4
+                                      // instead of 30.4 us for 2048 rows of 64 experts, 1024 -> 1408)
   __shared__ int s_wsum[WM * WN];
   __shared__ int s_wcost[WM * WN];
   __shared__ int s_share[kXcds + 1];  // first item of each XCD's share
@@ -178,6 +180,7 @@ void fp4_tile_kernel(const Fp4Args g) {
       const int tiles = div_up(hi - lo, BM);
       const int c = cost_of(hi - lo, tiles);
       s_start[e] = base;
+      s_beg[e] = lo;
       for (int q = 1; q < kXcds; ++q) {  // the shares that end inside this expert
         const int at = (int)((int64_t)ctotal * q / kXcds);
         if (at >= cbase && at < cbase + c)
@@ -188,6 +191,7 @@ void fp4_tile_kernel(const Fp4Args g) {
     }
     if (tid == NT - 1) {
       s_start[g.E] = total;
+      s_beg[g.E] = min(max(g.offsets[g.E], 0), g.R);
       s_share[kXcds] = total * per_tile;
     }
     __syncthreads();
@@ -215,7 +219,8 @@ void fp4_tile_kernel(const Fp4Args g) {
       t.e = lo;
       tiles = start(lo + 1) - start(lo);
       local = item - per_tile * start(lo);
-      fp4_segment(g, t.e, beg, end);
+      beg = s_beg[lo];  // (as fp4_segment)
+      end = max(beg, s_beg[lo + 1]);
     }
     constexpr int kGroup = 8;
     const int group = local / (kGroup * per_tile) * kGroup;
