@@ -311,6 +311,7 @@ hipError_t run_capacity(const moe_problem& p, int32_t* ids, float* w, uint8_t* k
                         const RankScratch& r, hipStream_t s, const uint8_t* candidates = nullptr) {
   hipError_t err = hipSuccess;
   if (p.capacity <= 0) return err;
+  if (capacity_direct(p)) return launch_capacity_direct(p, ids, candidates, w, keep, s);
   if ((err = launch_layout(p, ids, candidates, r.chunk_hist, r.chunk_base, r.cand_counts,
                            r.cand_offsets, nullptr, nullptr, r.cand_slot, s)) != hipSuccess)
     return err;

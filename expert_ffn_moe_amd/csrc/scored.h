@@ -14,6 +14,13 @@ namespace moe {
 hipError_t launch_router_logits(const moe_problem& p, const void* x, const void* wr, float* part,
                                 hipStream_t s);
 
+// ---- dispatch.hip
+// Capacity over the slots themselves, for few tokens (no layout, no scratch).
+bool capacity_direct(const moe_problem& p);
+hipError_t launch_capacity_direct(const moe_problem& p, const int32_t* ids,
+                                  const uint8_t* candidates, const float* topk_w, uint8_t* keep,
+                                  hipStream_t s);
+
 // ---- scored.hip
 // Selection from S planes [T, E] of fp32 logits, added in plane order (S = 1: the logits); the
 // sums are also written to logits_out if it is not NULL.

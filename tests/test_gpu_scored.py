@@ -229,3 +229,23 @@ def test_large_batch_capture_and_streams():
         assert all(torch.equal(a, q) for a, q in zip(got, (*out, dl)))
         if seed == 3:
             assert all(torch.equal(a, q) for a, q in zip(got, first))
+
+
+@pytest.mark.parametrize("kind", ["equal", "few", "normal", "wide"])
+@pytest.mark.parametrize("T", [1, 2, 256, 257, 1025, 8192, 8193, 13001])
+def test_capacity_of_one_crowded_expert(T, kind):
+    """Nearly every token chooses expert 2: 256 candidates are ranked, more are selected by digits,
+    8193 tokens and more through a layout, and 12288 candidates no longer fit on the chip."""
+    import oracle
+
+    m = moe()
+    g = torch.Generator().manual_seed(T)
+    x = {"equal": torch.zeros(T, 8), "few": torch.randint(0, 3, (T, 8), generator=g).float() / 4,
+         "normal": torch.randn(T, 8, generator=g), "wide": 40 * torch.randn(T, 8, generator=g)}[kind]
+    x[:, 2] += 6.0 * (torch.arange(T) % 29 != 0)
+    for C in sorted({1, (T + 1) // 2, max(1, T - 1), T}):
+        p = m.Problem(T=T, H=64, E=8, k=2, I=64, capacity=C)
+        for sc in (None, m.Scoring("softmax"), m.Scoring("sigmoid", scale=2.5)):
+            ids, w, keep = (m.route(p, x.cuda()) if sc is None else m.route_scored(p, x.cuda(), sc))
+            want = oracle.capacity(ids.cpu().numpy(), w.cpu().numpy(), 8, C)
+            assert (keep.cpu().numpy() == want).all(), (C, sc)
