@@ -118,6 +118,7 @@ void fp4_tile_kernel(const Fp4Args g) {
   constexpr int kABytes = BM * kSubs * 128, kBBytes = BN * 128;
   constexpr int kScA = kABytes + kBBytes, kScB = kScA + BM * 8;
   constexpr int kSlot = kScB + BN * 8;
+  constexpr int kMost = NT == 512 && !EIGHT && !GATHER ? 4 : 2;  // stages whose scales one load brings, see run
   static_assert(BM % kRpl == 0 && BM + BN <= NT && (kRpl == 64 || kRpl == 32), "");
   __shared__ __align__(1024) char smem[2 * kSlot];
   __shared__ int s_start[kMaxE + 1];  // M tiles before each expert
@@ -246,9 +247,9 @@ void fp4_tile_kernel(const Fp4Args g) {
   const uint8_t* a_ptr[GATHER ? BM / kRpl : 1];
   uint32_t a_off = 0, a_last = 0, b_off = 0, b_last[2] = {0, 0};
   const uint8_t* sc_ptr;  // this thread's row of scales
-  // Its words: 0, 1 of the stage whose scales are to be stored next, 2, 3 of the one after it where
-  // two were loaded at once
-  u32x4 sc;
+  // Its words: 0, 1 of the stage whose scales are to be stored next, 2 .. of those after it where
+  // two or four were loaded at once
+  uint32_t __attribute__((ext_vector_type(2 * kMost))) sc;
   const int pos = tid % 8, piece = pos ^ rows_swizzle(tid / 8);
   const uint32_t b_stride = (gated ? 32 : 64) * b_ld;  // from a wavefront column's rows to the next's
   // the row of scales this thread brings: of A, then of B (a thread behind them one again)
@@ -449,7 +450,8 @@ void fp4_tile_kernel(const Fp4Args g) {
     sb[0] = nb_[0];
     sb[1] = nb_[1];
   };
-  enum { kNone, kCopy, kCopyScales };  // what step 3 copies: a stage, with the scales of two
+  // What step 3 copies: nothing, a stage, a stage with the scales of that and the next 1 or 3.
+  enum { kNone, kCopy, kCopy2, kCopy4 };
   // Step S of a stage from `cur`; the fragments of the step after it are read meanwhile (of the
   // next stage behind step 3, with its scales), and with kCopy the copies of a whole stage are
   // issued into the slot that this stage no longer reads.
@@ -461,8 +463,9 @@ void fp4_tile_kernel(const Fp4Args g) {
     constexpr int kNext = (S + 1) % 4;
     const uint32_t so = (S == 3 ? slot ^ 1 : slot) * kSlot;
     const uint32_t la = COPY ? slot_lds(slot) : 0;
-    if constexpr (decltype(copy_c)::value == kCopyScales)
-      __builtin_memcpy(&sc, sc_ptr + cp_stage * kStageBlocks, 16);
+    if constexpr (decltype(copy_c)::value >= kCopy2)
+      __builtin_memcpy(&sc, sc_ptr + cp_stage * kStageBlocks,
+                       decltype(copy_c)::value == kCopy2 ? 16 : 32);
     if constexpr (S == 3) read_scales(so);
 #pragma unroll
     for (int m = 0; m < NM; ++m) {
@@ -627,8 +630,11 @@ void fp4_tile_kernel(const Fp4Args g) {
 #pragma unroll
       for (int m = 0; m < NM; ++m) read_a(f0, slot * kSlot, 0, m);
       // Stages behind whose barrier a whole stage of this same item is copied, without branches and
-      // by two: 16 bytes of a row's scales at a time (by one, a quarter of the traffic out of the
-      // L2 was lines of scales of which 8 bytes were used).
+      // by two: 16 bytes of a row's scales at a time, as every load fetches a line (by one, half of
+      // the requests to the L2 were for scales).  By four in the tall tile on rows of 4 bits in
+      // order: 16384 x 8192 x 8192 554 us instead of 575.  Not for a short reduction (8 stages: 109
+      // and 107 us), and not where the rows are gathered (their pointers leave no registers: 8192
+      // rows 1024 -> 4096 60 and 56 us) or hold 8 bits (65536 rows 4096 -> 4096 twice 1031 and 1011).
       const int whole = min(nb / kStageBlocks, cp_end);
       const int fast = cp_idx == idx ? max(whole - cp_stage, 0) / 2 * 2 : 0;
       const int stages = item.s1 - item.s0;
@@ -639,9 +645,9 @@ void fp4_tile_kernel(const Fp4Args g) {
         step(S2, slot, nm_c, No{});
         wait_copies();
         store_scales(slot ^ 1);
-        if constexpr (decltype(copy_c)::value == kCopy) {  // the second of two
-          sc[0] = sc[2];
-          sc[1] = sc[3];
+        if constexpr (decltype(copy_c)::value == kCopy) {  // not the first of its load
+#pragma unroll
+          for (int i = 2; i < 2 * kMost; ++i) sc[i - 2] = sc[i];
         }
         wait_copies();
         block_barrier();
@@ -650,8 +656,16 @@ void fp4_tile_kernel(const Fp4Args g) {
         copies_done();
         slot ^= 1;
       };
+      if constexpr (kMost == 4) {
+        for (const int fours = nst >= 16 ? fast / 4 * 4 : 0; s < fours; s += 4) {
+          stage(std::integral_constant<int, kCopy4>{});
+          stage(std::integral_constant<int, kCopy>{});
+          stage(std::integral_constant<int, kCopy>{});
+          stage(std::integral_constant<int, kCopy>{});
+        }
+      }
       for (; s < fast; s += 2) {
-        stage(std::integral_constant<int, kCopyScales>{});
+        stage(std::integral_constant<int, kCopy2>{});
         stage(std::integral_constant<int, kCopy>{});
       }
       // The others: a partial stage, the next item's first ones, or nothing left to copy.

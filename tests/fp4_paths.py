@@ -55,4 +55,9 @@ PATHS = [
           wild=True, residual=True)),
     ((STREAM, 1), (STREAM, 1), dict(counts=[1] + [0] * 1022 + [40], K=64, N=40)),
     ((STREAM, 1), (STREAM, 1), dict(counts=[0] * 200 + [70] + [0] * 100, K=288, N=72)),
+    # scales by four stages: 16 stages, 17 with a partial one, 21 with several items of a block
+    ((TILE256, 1), (TILE256, 1), dict(counts=[700], K=4096, N=16400)),
+    ((TILE256, 1), (TILE256, 1), dict(counts=[390, 301], K=4320, N=16400, bias=True, behind=9)),
+    ((TILE256, 1), (TILE256, 1),
+     dict(counts=[1030], K=5376, N=16400, gated=True, act="silu", front=3)),
 ]
