@@ -305,7 +305,8 @@ size_t natural_w_bytes(const moe_problem& p) {  // one natural weight set [E, H,
   return (size_t)p.E * p.H * p.I * (p.w_dtype == MOE_F32 ? 4 : 2);
 }
 
-// Capacity after the selection: candidate layout + radix select (no-op without a cap).
+// Capacity after the selection: from the slots themselves, or a candidate layout + radix select
+// (no-op without a cap).
 // candidates: NULL (every slot), or keep flags of the slots that count.
 hipError_t run_capacity(const moe_problem& p, int32_t* ids, float* w, uint8_t* keep,
                         const RankScratch& r, hipStream_t s, const uint8_t* candidates = nullptr) {
