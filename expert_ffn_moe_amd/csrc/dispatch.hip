@@ -339,8 +339,8 @@ __global__ __launch_bounds__(kCapThreads) void capacity_select_kernel(
 constexpr int kCapDirectTokens = 8192;
 constexpr int kCapRanked = 256;
 __global__ __launch_bounds__(kCapThreads) void capacity_direct_kernel(
-    const int32_t* __restrict__ ids, const uint8_t* __restrict__ candidates,
-    const float* __restrict__ w, int slots, int k, int C, uint8_t* __restrict__ keep) {
+    const int32_t* __restrict__ ids, const uint8_t* candidates, const float* __restrict__ w,
+    int slots, int k, int C, uint8_t* keep) {  // (candidates may be keep)
   __shared__ uint64_t s_keys[kCapDirectTokens];  // (an expert is a token's once)
   __shared__ int32_t s_slot[kCapDirectTokens];
   __shared__ CapShared sh;
