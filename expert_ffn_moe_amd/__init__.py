@@ -611,6 +611,11 @@ class GroupedProblem:
         object.__setattr__(self, "_c", c)
         object.__setattr__(self, "_ref", ctypes.byref(c))
         object.__setattr__(self, "_ws_bytes", {})
+        # the shapes of grouped_linear_fp4's tensors, which small calls should not build again:
+        # w codes, w scales, bias, y; then x codes in 4 bits, in 8 and x scales, [R, .] and [T, .]
+        n, K, q = (self.E, self.N), self.K, self.K // QBLOCK
+        x = [((m, K // 2), (m, K), (m, q)) for m in (self.R, self.x_tokens)]
+        object.__setattr__(self, "_fp4", (n + (K // 2,), n + (q,), n, (self.R, self.N), *x))
 
     def __reduce__(self):  # a copy derives its own: the C struct's reference cannot be copied
         return type(self), (self.R, self.K, self.N, self.E, self.T)
@@ -907,13 +912,13 @@ def route_scored_backward(p: Problem, logits, scoring: Scoring, topk_ids, topk_w
 
 # ---- microscaled 4-bit values (see moe_quantize_fp4 and the calls after it in include/moe.h)
 def _fp4_shapes(shape):
+    """(shape of the codes, of the scales) of values [..., C]"""
     if len(shape) < 2:
         raise ValueError("rows of 32-value blocks are needed: at least 2-D")
-    if shape[-1] % QBLOCK or shape[-1] == 0:
-        raise ValueError(f"the last dimension must be a positive multiple of {QBLOCK}, not "
-                         f"{shape[-1]}")
-    lead = tuple(shape[:-1])
-    return lead + (shape[-1] // 2,), lead + (shape[-1] // QBLOCK,)
+    *lead, cols = shape
+    if cols % QBLOCK or cols == 0:
+        raise ValueError(f"the last dimension must be a positive multiple of {QBLOCK}, not {cols}")
+    return (*lead, cols // 2), (*lead, cols // QBLOCK)
 
 
 def quantize_fp4(x, live_rows=None, out=None):
@@ -921,12 +926,13 @@ def quantize_fp4(x, live_rows=None, out=None):
     low half of byte i, scales [..., C/32] u8).  live_rows: an i32 tensor of one element; rows
     from there on are neither read nor written."""
     u8, bf = torch.uint8, torch.bfloat16
-    cs, ss = _fp4_shapes(x.shape)
-    dev = _first(x, "x", x.shape, bf)
+    shape = x.shape
+    cs, ss = _fp4_shapes(shape)
+    dev = _first(x, "x", shape, bf)
     codes, scales = out if out is not None else (_empty(cs, u8, x.device),
                                                  _empty(ss, u8, x.device))
-    cols = x.shape[-1]
-    _launch("moe_quantize_fp4", dev, _arg(x, "x", x.shape, bf, dev), x.numel() // cols, cols,
+    cols = shape[-1]
+    _launch("moe_quantize_fp4", dev, _arg(x, "x", shape, bf, dev), x.numel() // cols, cols,
             _arg(live_rows, "live_rows", (1,), torch.int32, dev),
             _arg(codes, "codes", cs, u8, dev), _arg(scales, "scales", ss, u8, dev))
     return codes, scales
@@ -935,7 +941,8 @@ def quantize_fp4(x, live_rows=None, out=None):
 def dequantize_fp4(codes, scales, live_rows=None, out=None):
     """The bf16 values [..., C] of a 4-bit form (exact); live_rows as quantize_fp4."""
     u8, bf = torch.uint8, torch.bfloat16
-    shape = tuple(codes.shape[:-1]) + (2 * codes.shape[-1],)
+    *lead, half = codes.shape
+    shape = (*lead, 2 * half)
     cs, ss = _fp4_shapes(shape)
     dev = _first(codes, "codes", cs, u8)
     values = _empty(shape, bf, codes.device) if out is None else out
@@ -963,14 +970,6 @@ def quantize_fp4_weights(w, out=None):
     return codes, scales
 
 
-def _fp4_weights(p: GroupedProblem, w, bias, what: str, index: int) -> MoeFp4Weights:
-    codes, scales = w
-    u8 = torch.uint8
-    return MoeFp4Weights(_arg(codes, f"{what} codes", (p.E, p.N, p.K // 2), u8, index),
-                         _arg(scales, f"{what} scales", (p.E, p.N, p.K // QBLOCK), u8, index),
-                         _arg(bias, f"{what} bias", (p.E, p.N), torch.bfloat16, index))
-
-
 def grouped_linear_fp4(p: GroupedProblem, x, w, offsets=None, up=None, bias=None, up_bias=None,
                        act: str = "none", residual=None, row_token=None, out=None, ws=None):
     """y[r] = act(x[r] w[e] + bias[e]) * (x[r] up[e] + up_bias[e]) + residual[r] for the rows of
@@ -978,22 +977,28 @@ def grouped_linear_fp4(p: GroupedProblem, x, w, offsets=None, up=None, bias=None
     quantize_fp4_weights; x: (codes, scales) of quantize_fp4 (codes [R, K/2]) or quantize_fp8
     ([R, K]), [T, .] read through row_token.  Returns y [R, N]; rows behind the last expert's are
     left as they were."""
-    bf, u8, R, K, N = torch.bfloat16, torch.uint8, p.R, p.K, p.N
-    codes, scales = x
-    rows = R if row_token is None else p.x_tokens
-    eight = isinstance(codes, torch.Tensor) and codes.dim() == 2 and codes.shape[1] == K
-    xs = (rows, K if eight else K // 2)
-    dev = _first(codes, "x codes", xs, u8)
+    bf, u8 = torch.bfloat16, torch.uint8
+    wcs, wss, bs, ys, xr, xt = p._fp4
+    four, xs, xss = xr if row_token is None else xt
+    (codes, scales), (w_codes, w_scales) = x, w
+    dev = _first(codes, "x codes", four, u8)
+    eight = codes.shape == xs
     if up is None and up_bias is not None:
         raise ValueError("up_bias needs up")
-    y = _empty((R, N), bf, codes.device) if out is None else out
-    wc = _fp4_weights(p, w, bias, "w", dev)
-    uc = ctypes.byref(_fp4_weights(p, up, up_bias, "up", dev)) if up is not None else None
+    y = _empty(ys, bf, codes.device) if out is None else out
+    wc = MoeFp4Weights(_arg(w_codes, "w codes", wcs, u8, dev),
+                       _arg(w_scales, "w scales", wss, u8, dev), _arg(bias, "w bias", bs, bf, dev))
+    uc = None
+    if up is not None:
+        up_codes, up_scales = up
+        uc = MoeFp4Weights(_arg(up_codes, "up codes", wcs, u8, dev),
+                           _arg(up_scales, "up scales", wss, u8, dev),
+                           _arg(up_bias, "up bias", bs, bf, dev))
     ws, wsp, wsn = _grouped_ws(p, OP_GROUPED_FP4, ws, codes)
     _launch("moe_grouped_linear_fp4", dev, p._ref, MOE_FP8 if eight else MOE_FP4,
-            _arg(codes, "x codes", xs, u8, dev),
-            _arg(scales, "x scales", (rows, K // QBLOCK), u8, dev),
-            _arg(row_token, "row_token", (R,), torch.int32, dev), _offsets_arg(p, offsets, dev),
-            ctypes.byref(wc), uc, _act(act), _arg(residual, "residual", (R, N), bf, dev),
-            _arg(y, "out", (R, N), bf, dev), wsp, wsn)
+            _arg(codes, "x codes", xs if eight else four, u8, dev),
+            _arg(scales, "x scales", xss, u8, dev),
+            _arg(row_token, "row_token", (p.R,), torch.int32, dev), _offsets_arg(p, offsets, dev),
+            wc, uc, _act(act), _arg(residual, "residual", ys, bf, dev),
+            _arg(y, "out", ys, bf, dev), wsp, wsn)
     return y
