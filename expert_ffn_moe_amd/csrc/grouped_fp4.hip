@@ -113,8 +113,8 @@ struct Item {
 // the whole time of 16384 x 8192 x 8192.  3.2 PFLOP/s on ragged rows (131072 rows of 256 experts, 7168
 // -> 2048 twice, 2.4 ms), 4.0 on that dense product; the instruction alone reaches 8.2 (fp4, 32 x 32 x
 // 64; 16 x 16 x 128: 6.1) and 4.5 with x in 8 bits.  Few rows per expert: the weights' bytes, 5.7 TB/s
-// (1024 rows of 256 experts, 7168 -> 2048 twice: 690 us).  Few stages: latency, the first two stages of an item being
-// copied beside the last ones of the item before it.
+// (1024 rows of 256 experts, 7168 -> 2048 twice: 690 us).  Few stages: latency, the first two stages
+// of an item being copied beside the last ones of the item before it.
 template <bool EIGHT, bool GATHER, int BM, int WM, int WN, bool ONCE = false>
 __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2, 2)))
 void fp4_tile_kernel(const Fp4Args g) {
@@ -126,7 +126,8 @@ void fp4_tile_kernel(const Fp4Args g) {
   constexpr int kABytes = BM * kSubs * 128, kBBytes = BN * 128;
   constexpr int kScA = kABytes + kBBytes, kScB = kScA + BM * 8;
   constexpr int kSlot = kScB + BN * 8;
-  constexpr int kMost = NT == 512 && !EIGHT && !GATHER ? 4 : 2;  // stages whose scales one load brings, see run
+  // stages whose scales one load brings, see run
+  constexpr int kMost = NT == 512 && !EIGHT && !GATHER ? 4 : 2;
   static_assert(BM % kRpl == 0 && BM + BN <= NT && (kRpl == 64 || kRpl == 32), "");
   __shared__ __align__(1024) char smem[2 * kSlot];
   __shared__ int s_start[kMaxE + 1];  // M tiles before each expert

@@ -314,10 +314,10 @@ __device__ __forceinline__ void sort_keys(uint32_t* v) {
 // A row of 16 lanes takes a token, a lane EPL consecutive experts: four tokens to a wavefront, every
 // reduction inside a row.  Each lane sorts its keys first, so that a round of the choice is the
 // maximum of the lanes' heads and the winner moves on to its next one.  For k <= 8 (a lane keeps 8
-// keys) of up to 256 experts: 16384 tokens, 8 of 256 by groups, 16.5 to 17.5 us a call, where a wavefront for
-// a token, in 64 bits throughout, took 38.6.  Its 16.8 MB are 3.7 us at the rate of a copy; the four
-// wavefronts of a SIMD all load, then all compute (about 7 us of instructions), so that the two
-// add up, with the launch's own start and end.
+// keys) of up to 256 experts: 16384 tokens, 8 of 256 by groups, 16.5 to 17.5 us a call, where a
+// wavefront for a token, in 64 bits throughout, took 38.6.  Its 16.8 MB are 3.7 us at the rate of a
+// copy; the four wavefronts of a SIMD all load, then all compute (about 7 us of instructions), so
+// that the two add up, with the launch's own start and end.
 //
 // In 32 bits a key is the order-preserving bits of the value, the last ones replaced by the value's
 // place in its lane.  Bounds: a sigmoid from the hardware's exponential and reciprocal (1 ulp
