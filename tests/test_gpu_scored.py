@@ -249,3 +249,39 @@ def test_capacity_of_one_crowded_expert(T, kind):
             ids, w, keep = (m.route(p, x.cuda()) if sc is None else m.route_scored(p, x.cuda(), sc))
             want = oracle.capacity(ids.cpu().numpy(), w.cpu().numpy(), 8, C)
             assert (keep.cpu().numpy() == want).all(), (C, sc)
+
+
+# (more than 8192 tokens, or more than 2^24 slots times experts: capacity through a layout)
+LAYOUT_CASES = [
+    (9001, 16, 6, "softmax", 4, 3, "top2", "out", True, 1.0, 1500, "masked"),
+    (8192, 300, 8, "sigmoid", 1, 1, "max", "normal", False, 2.5, 190, "masked"),
+]
+
+
+@pytest.mark.parametrize("c", LAYOUT_CASES, ids=str)
+def test_capacity_through_a_layout(c):
+    """Slots whose expert is out do not count there either; captured and replayed, too."""
+    m, p, sc, x, bias, (ids, w, keep) = setup(c)
+    x, bias = x.cuda(), bias.cuda()
+    ws = m.workspace(p, m.OP_ROUTE)
+    out = tuple(torch.empty(p.T, p.k, dtype=t, device="cuda")
+                for t in (torch.int32, torch.float32, torch.uint8))
+    m.route_scored(p, x, sc, bias=bias, out=out, ws=ws)
+    assert (out[0].cpu().numpy() == ids).all() and (out[2].cpu().numpy() == keep).all()
+    assert (keep == 0).sum() > (w == 0).sum() > 0  # some by the capacity, some that are out
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        m.route_scored(p, x, sc, bias=bias, out=out, ws=ws)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        m.route_scored(p, x, sc, bias=bias, out=out, ws=ws)
+    for step in range(3):
+        x.copy_(x.roll(1, 0))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in out]
+        want = m.route_scored(p, x, sc, bias=bias)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
