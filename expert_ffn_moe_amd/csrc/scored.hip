@@ -325,7 +325,9 @@ __device__ __forceinline__ void sort_keys(uint32_t* v) {
 // sum, 2^-23 for the reciprocal), with the bias 2^-24 of the sum more; a softmax by at most 2^-19
 // (its total by 25 2^-24 of itself).  Two values are told apart where they differ by more than
 // the sum of their bounds, taken as eps (1 + |value|) with eps 2^-20 (2^-17 for the softmax) and
-// EPL 2^-22 |value| for the keys, group values of two scores with twice the first.
+// EPL 2^-22 |value| for the keys.  A group's sum of two is held to its parts, for large biases
+// may cancel in it: each is off by 2^-22 (1 + |part|) (2^-19 + 2^-24 |part|), the sum by 2^-24 of
+// itself more, two groups by less than twice eps (1 + |part| + |part|) of the larger one together.
 template <int EPL, bool SOFTMAX>  // E <= 16 * EPL
 __global__ __launch_bounds__(256) void scored_rows_kernel(const ScoredArgs a) {
   constexpr int D = EPL < 8 ? EPL : 8;  // keys a lane keeps
@@ -396,16 +398,19 @@ __global__ __launch_bounds__(256) void scored_rows_kernel(const ScoredArgs a) {
     if (a.span > 1) merge2(v1, v2, dpp_f<kDppQuadXor1>(v1), dpp_f<kDppQuadXor1>(v2));
     if (a.span > 2) merge2(v1, v2, dpp_f<kDppQuadXor2>(v1), dpp_f<kDppQuadXor2>(v2));
     if (a.span > 4) merge2(v1, v2, dpp_f<kDppRowHalfMirror>(v1), dpp_f<kDppRowHalfMirror>(v2));
-    const float mine = top2 && is_in(v2) ? v1 + v2 : v1;
+    const bool sum = top2 && is_in(v2);
+    const float mine = sum ? v1 + v2 : v1;
+    const float size = fabsf(v1) + (sum ? fabsf(v2) : 0.0f);
     // (ordered by the logits themselves only equal groups are close)
-    const float near = scores ? 2.0f * eps * (1.0f + fabsf(mine)) : 0.0f;
+    const float near = scores ? 2.0f * eps * (1.0f + size) : 0.0f;
     int ahead = 0, close = 0;
     for (int o = 0; o < a.n_group; ++o) {
       const float v = from_lane(mine, (lane & 48) + o * a.span);
       ahead += v > mine;
       close += fabsf(v - mine) <= near;
     }
-    unsure = close > 1 && l16 < a.n_group * a.span;  // (each is close to itself)
+    // (each is close to itself; parts that pass the range together are left to 64 bits)
+    unsure = (close > 1 || (sum && size > kBig)) && l16 < a.n_group * a.span;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) c[i] = ahead < a.topk_group ? c[i] : -INFINITY;
   }
