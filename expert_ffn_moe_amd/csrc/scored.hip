@@ -409,8 +409,10 @@ __global__ __launch_bounds__(256) void scored_rows_kernel(const ScoredArgs a) {
       ahead += v > mine;
       close += fabsf(v - mine) <= near;
     }
-    // (each is close to itself; parts that pass the range together are left to 64 bits)
-    unsure = (close > 1 || (sum && size > kBig)) && l16 < a.n_group * a.span;
+    // (each is close to itself; parts that pass the range together are left to 64 bits; a group that
+    // is wholly out, -inf, is behind the others and close to none: with one group out 16384 tokens,
+    // 8 of 256, took 54 us instead of 18 while it counted)
+    unsure = ((close > 1 && is_in(v1)) || (sum && size > kBig)) && l16 < a.n_group * a.span;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) c[i] = ahead < a.topk_group ? c[i] : -INFINITY;
   }

@@ -76,3 +76,26 @@ def test_two_groups_beyond_the_range():
     check(make_logits(50, 64, 1), 3, "sigmoid", b, 2, 1)
     b[32:34], b[0:2] = b[0:2].clone(), b[32:34].clone()
     check(make_logits(50, 64, 1), 3, "sigmoid", b, 2, 1)
+
+
+@pytest.mark.parametrize("kind", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("group_score", ["max", "top2"])
+@pytest.mark.parametrize("by", ["logits", "bias", "logits alone"])
+@pytest.mark.parametrize("E,G", SHAPES)
+def test_groups_that_are_wholly_out(E, G, by, group_score, kind):
+    """They are behind the others, take no part where enough are left, and fill the last slots (with
+    their lowest experts, in the taken groups) where not."""
+    T, size = 100, E // G
+    for gone in sorted({1, G // 2, G - 1, G}):
+        x = make_logits(T, E, gone)
+        b = None if by == "logits alone" else 0.1 * torch.randn(
+            E, generator=torch.Generator().manual_seed(gone))
+        out = torch.randperm(G, generator=torch.Generator().manual_seed(E))[:gone]
+        at = (out[:, None] * size + torch.arange(size)).reshape(-1)
+        if by == "bias":
+            b[at] = -INF
+        else:
+            x[:, at] = -INF
+            x[1, at[0]] = 0.5  # one of a group is there after all
+        for taken in sorted({1, max(1, G // 2), G - 1}):
+            check(x, 3, kind, b, G, taken, group_score)
