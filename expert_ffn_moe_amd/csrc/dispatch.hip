@@ -505,8 +505,11 @@ hipError_t launch_layout(const moe_problem& p, const int32_t* ids, const uint8_t
 bool capacity_direct(const moe_problem& p) {
   // Whole call with capacity T k / E, this way and by a layout: 4096 tokens, 8 of 128 experts 15.3
   // and 22.2 us; 8192 tokens, 8 of 256 22.4 and 26.1, skewed 28.6 and 32.7.  Every block reads every
-  // slot, so the time grows with T k E, and beyond 2^24 the layout catches up.
-  return p.T <= kCapDirectTokens && (int64_t)p.T * p.k * p.E <= 1 << 24;
+  // slot, so the time grows with T k E, and beyond 2^24 the layout catches up; with few experts it
+  // grows with the slots: 8192 tokens, 12 of 128 28.8 and 29.3 us, skewed 36.5 and 37.5; 16 of 128
+  // 35.3 and 34.3, skewed 45.6 and 43.5; 32 of 32 65 and 41.
+  const int64_t slots = (int64_t)p.T * p.k;
+  return p.T <= kCapDirectTokens && slots <= 12 * kCapDirectTokens && slots * p.E <= 1 << 24;
 }
 
 hipError_t launch_capacity_direct(const moe_problem& p, const int32_t* ids,

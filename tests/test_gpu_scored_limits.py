@@ -99,3 +99,23 @@ def test_groups_that_are_wholly_out(E, G, by, group_score, kind):
             x[1, at[0]] = 0.5  # one of a group is there after all
         for taken in sorted({1, max(1, G // 2), G - 1}):
             check(x, 3, kind, b, G, taken, group_score)
+
+
+# T, E, k on both sides of the rules of the capacity's two ways: 8192 tokens, 98304 slots, 2^24 slots
+# times experts
+@pytest.mark.parametrize("T,E,k", [(8192, 32, 12), (8192, 32, 13), (3100, 40, 32), (3000, 40, 32),
+                                   (8192, 16, 16), (8191, 34, 32), (8192, 170, 12), (8192, 171, 12)])
+def test_capacity_by_slots_and_through_a_layout(T, E, k):
+    import oracle
+
+    m = moe()
+    x = make_logits(T, E, k)
+    for skew in (0, 2):
+        xs = x + skew * torch.randn(E, generator=torch.Generator().manual_seed(E))
+        for C in (1, max(1, T * k // E), T - 1):
+            p = m.Problem(T=T, H=64, E=E, k=k, I=64, capacity=C)
+            for sc in (None, m.Scoring("sigmoid", scale=2.5)):
+                ids, w, keep = (m.route(p, xs.cuda()) if sc is None
+                                else m.route_scored(p, xs.cuda(), sc))
+                want = oracle.capacity(ids.cpu().numpy(), w.cpu().numpy(), E, C)
+                assert (keep.cpu().numpy() == want).all(), (C, sc)
