@@ -238,77 +238,88 @@ constexpr int kCapThreads = 1024;
 constexpr int kCapLdsKeys = 12288;  // candidates whose keys are held in LDS (96 KiB)
 
 struct CapShared {
-  unsigned long long low, high;
+  uint64_t low[kCapThreads / 64], high[kCapThreads / 64];
   uint32_t hist[256];
   int sel, need, done;
 };
 
-// The prefix p for which the keys >= p are exactly the C largest of cnt > C keys: digits of 8 bits,
-// from the highest bit in which two keys differ (the weights' exponents hardly do, and a digit that
-// all keys share is counted by as many atomics on one address).
+// One digit of the boundary key, bits shift .. shift + 7: of the keys that agree with prefix in mask,
+// the need-th largest decides.  true: the keys >= prefix are exactly the largest that were asked for.
+template <class KeyAt>
+__device__ __forceinline__ bool cap_digit(int cnt, KeyAt key_at, int shift, int& need,
+                                          uint64_t& mask, uint64_t& prefix, CapShared& sh) {
+  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+  if (tid < 256) sh.hist[tid] = 0;
+  __syncthreads();
+  for (int i = tid; i < cnt; i += kCapThreads) {
+    const uint64_t key = key_at(i);
+    if ((key & mask) == prefix) atomicAdd(&sh.hist[(key >> shift) & 255u], 1u);
+  }
+  __syncthreads();
+  // The boundary digit: the largest d with (keys above d) < need <= (keys at or above d).
+  // Wavefront 0, lane l holding digits 255 - 4l .. 252 - 4l (descending).
+  if (wave == 0) {
+    uint32_t h[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) h[q] = sh.hist[255 - (4 * lane + q)];
+    const int lsum = (int)(h[0] + h[1] + h[2] + h[3]);
+    int above = wave_inclusive_scan(lsum) - lsum;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      if (above < need && above + (int)h[q] >= need) {  // exactly one lane and q
+        sh.sel = 255 - (4 * lane + q);
+        sh.need = need - above;
+        sh.done = ((int)h[q] == need - above);
+      }
+      above += (int)h[q];
+    }
+  }
+  __syncthreads();
+  const int sel = sh.sel;
+  need = sh.need;
+  const int done = sh.done;
+  prefix |= (uint64_t)sel << shift;
+  mask |= (uint64_t)0xFF << shift;
+  return done;  // block-uniform
+  // (the barrier at the top of the next digit orders these reads before hist is cleared)
+}
+
+// The prefix p for which the keys >= p are exactly the C largest of cnt > C keys (its lower bits are
+// zero), by digits from the top.  Unrolled: the first ones then need no token, whose division is
+// most of building a key (100000 tokens, 4 of 64 experts, skewed: 167 us in a loop, 136).
 template <class KeyAt>
 __device__ __forceinline__ uint64_t cap_boundary(int cnt, int C, KeyAt key_at, CapShared& sh) {
-  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
-  if (tid == 0) {
-    sh.low = ~0ull;
-    sh.high = 0;
-  }
-  __syncthreads();
-  unsigned long long low = ~0ull, high = 0;
-  for (int i = tid; i < cnt; i += kCapThreads) {
-    const unsigned long long key = key_at(i);
-    low = min(low, key);
-    high = max(high, key);
-  }
-  for (int o = 32; o > 0; o >>= 1) {
-    low = min(low, __shfl_xor(low, o));
-    high = max(high, __shfl_xor(high, o));
-  }
-  if (lane == 0) {
-    atomicMin(&sh.low, low);
-    atomicMax(&sh.high, high);
-  }
-  __syncthreads();
-  const int top = 63 - __clzll((long long)(sh.low ^ sh.high));  // (keys differ: cnt > C >= 1)
-  uint64_t mask = top == 63 ? 0 : ~0ull << (top + 1);
-  uint64_t prefix = sh.high & mask;
+  uint64_t prefix = 0, mask = 0;
   int need = C;
-  for (int shift = max(top - 7, 0);; shift = max(shift - 8, 0)) {
-    if (tid < 256) sh.hist[tid] = 0;
-    __syncthreads();
-    for (int i = tid; i < cnt; i += kCapThreads) {
-      const uint64_t key = key_at(i);
-      if ((key & mask) == prefix) atomicAdd(&sh.hist[(key >> shift) & 255u], 1u);
-    }
-    __syncthreads();
-    // The boundary digit: the largest d with (keys above d) < need <= (keys at or above d).
-    // Wavefront 0, lane l holding digits 255 - 4l .. 252 - 4l (descending).
-    if (wave == 0) {
-      uint32_t h[4];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) h[q] = sh.hist[255 - (4 * lane + q)];
-      const int lsum = (int)(h[0] + h[1] + h[2] + h[3]);
-      int above = wave_inclusive_scan(lsum) - lsum;
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        if (above < need && above + (int)h[q] >= need) {  // exactly one lane and q
-          sh.sel = 255 - (4 * lane + q);
-          sh.need = need - above;
-          sh.done = ((int)h[q] == need - above);
-        }
-        above += (int)h[q];
-      }
-    }
-    __syncthreads();
-    const int sel = sh.sel;
-    need = sh.need;
-    const int done = sh.done;
-    prefix |= (uint64_t)sel << shift;
-    mask |= (uint64_t)0xFF << shift;
-    if (done || shift == 0) break;  // block-uniform; the last digit ends it, keys being unique
-    // (the barrier at the top of the next pass orders these reads before hist is cleared)
+  for (int shift = 56; shift >= 0; shift -= 8)
+    if (cap_digit(cnt, key_at, shift, need, mask, prefix, sh)) break;
+  return prefix;
+}
+
+// The same from the highest bit in which two keys differ, for keys at hand in LDS: the weights'
+// exponents hardly do, and a digit that all keys share is counted by as many atomics on one address.
+// low, high: the least and the largest of the keys that this thread has built (~0, 0 for none).
+template <class KeyAt>
+__device__ __forceinline__ uint64_t cap_boundary(int cnt, int C, KeyAt key_at, uint64_t low,
+                                                 uint64_t high, CapShared& sh) {
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  low = ~wave_max_u64(~low);
+  high = wave_max_u64(high);
+  if (lane == 0) {
+    sh.low[wave] = low;
+    sh.high[wave] = high;
   }
-  return prefix;  // (its lower bits are zero)
+  __syncthreads();
+  low = ~row_max_u64(~sh.low[lane & 15]);
+  high = row_max_u64(sh.high[lane & 15]);
+  const int top = 63 - __clzll((long long)(low ^ high));  // (keys differ: cnt > C >= 1)
+  uint64_t mask = top == 63 ? 0 : ~0ull << (top + 1);
+  uint64_t prefix = high & mask;
+  int need = C;
+  for (int shift = max(top - 7, 0);; shift = max(shift - 8, 0))  // (keys are unique)
+    if (cap_digit(cnt, key_at, shift, need, mask, prefix, sh) || shift == 0) break;
+  return prefix;
 }
 
 __global__ __launch_bounds__(kCapThreads) void capacity_select_kernel(
@@ -324,10 +335,22 @@ __global__ __launch_bounds__(kCapThreads) void capacity_select_kernel(
   const int32_t* slots = cand_slot + cand_offsets[e];
   // keys are built once into LDS when they fit; otherwise every pass rebuilds them
   const bool in_lds = cnt <= kCapLdsKeys;  // block-uniform
+  uint64_t low = ~0ull, high = 0, prefix;
   if (in_lds)
-    for (int i = tid; i < cnt; i += kCapThreads) s_keys[i] = cap_key(w, slots[i], k);
+    for (int i = tid; i < cnt; i += kCapThreads) {
+      const uint64_t key = cap_key(w, slots[i], k);
+      s_keys[i] = key;
+      low = min(low, key);
+      high = max(high, key);
+    }
   auto key_at = [&](int i) { return in_lds ? s_keys[i] : cap_key(w, slots[i], k); };
-  const uint64_t prefix = cap_boundary(cnt, C, key_at, sh);
+  // (joining low and high takes longer than the digits that it saves where those have one key a
+  // thread: 8192 tokens, 8 of 512 experts 9.3 us with it, 7.9 without; 16384 tokens, 2 of 8 experts
+  // 23.7 and 24.8 us a call)
+  if (in_lds && cnt > kCapThreads)
+    prefix = cap_boundary(cnt, C, key_at, low, high, sh);
+  else
+    prefix = cap_boundary(cnt, C, key_at, sh);
   for (int i = tid; i < cnt; i += kCapThreads)
     if (key_at(i) < prefix) keep[slots[i]] = 0;
 }
@@ -368,6 +391,7 @@ __global__ __launch_bounds__(kCapThreads) void capacity_direct_kernel(
   __syncthreads();
   const int found = min(s_count, kCapDirectTokens);
   if (found <= C) return;  // block-uniform
+  uint64_t low = ~0ull, high = 0;
   for (int i = tid; i < found; i += kCapThreads) {  // (their weights are read side by side)
     const int s = s_found[i];
     const uint64_t key = cap_key(w, s, k);
@@ -375,6 +399,8 @@ __global__ __launch_bounds__(kCapThreads) void capacity_direct_kernel(
       const int at = atomicAdd(&s_taken, 1);
       s_slot[at] = s;
       s_keys[at] = key;
+      low = min(low, key);
+      high = max(high, key);
     }
   }
   __syncthreads();
@@ -389,7 +415,7 @@ __global__ __launch_bounds__(kCapThreads) void capacity_direct_kernel(
     }
     return;
   }
-  const uint64_t prefix = cap_boundary(cnt, C, [&](int i) { return s_keys[i]; }, sh);
+  const uint64_t prefix = cap_boundary(cnt, C, [&](int i) { return s_keys[i]; }, low, high, sh);
   for (int i = tid; i < cnt; i += kCapThreads)
     if (s_keys[i] < prefix) keep[s_slot[i]] = 0;
 }
