@@ -567,8 +567,9 @@ __global__ __launch_bounds__(256) void scored_bwd_kernel(const ScoredBwdArgs a) 
   const double w = mine ? (double)a.w[o] : 0.0;
   const double d = w != 0.0 ? (double)a.dw[o] : 0.0;
   const int first = lane / a.k * a.k;
+  const bool softmax = a.score == MOE_SCORE_SOFTMAX;
   double D = 0.0, sum = 0.0;
-  if (a.renorm || a.score == MOE_SCORE_SOFTMAX) {
+  if (a.renorm || softmax) {
     for (int j = 0; j < a.k; ++j) {
       D += __shfl(w * d, first + j, 64);
       sum += __shfl(w, first + j, 64);
@@ -576,10 +577,16 @@ __global__ __launch_bounds__(256) void scored_bwd_kernel(const ScoredBwdArgs a) 
   }
   if (a.renorm) D = sum != 0.0 ? D / sum : 0.0;
   double g = w * (a.renorm ? d - D : d);
-  if (a.score == MOE_SCORE_SIGMOID && w != 0.0 && (unsigned)e < (unsigned)a.E)
-    g *= sigmoid64(-(double)fminf(a.logits[(size_t)(t0 + lane / a.k) * a.E + e], kBig));
+  // (+inf moves nothing: the sigmoid's slope is 0 there; beside it the softmax leaves weights to its
+  // like alone, all equal, whose sum is exact, so that few tokens read their logits for it)
+  const int n = __popcll(__ballot(w != 0.0) >> first & ((1ull << a.k) - 1));
+  if (w != 0.0 && (!softmax || w * n == sum) && (unsigned)e < (unsigned)a.E) {
+    const float l = a.logits[(size_t)(t0 + lane / a.k) * a.E + e];
+    if (!softmax) g *= sigmoid64(-(double)fminf(l, kBig));
+    else if (l == INFINITY) g = 0.0;
+  }
   const float gf = (float)g;
-  const bool dense = a.score == MOE_SCORE_SOFTMAX && !a.renorm;
+  const bool dense = softmax && !a.renorm;
   for (int q = 0; q < nt; ++q) {
     const size_t row = (size_t)(t0 + q) * a.E;
     float v[EPL];
@@ -590,8 +597,10 @@ __global__ __launch_bounds__(256) void scored_bwd_kernel(const ScoredBwdArgs a) 
       float l[EPL];
       load_row<EPL>(a.logits + row, a.E, lane, a.vec, -INFINITY, l);
       float m = -kBig;
+      uint32_t moves = 0;  // values below +inf
 #pragma unroll
       for (int i = 0; i < EPL; ++i) {
+        moves |= (uint32_t)(l[i] < INFINITY) << i;
         l[i] = tamed(l[i]);
         m = fmaxf(m, l[i]);
       }
@@ -614,7 +623,7 @@ __global__ __launch_bounds__(256) void scored_bwd_kernel(const ScoredBwdArgs a) 
           if (lane * EPL + i == ej) p[i] += gj;
       }
 #pragma unroll
-      for (int i = 0; i < EPL; ++i) v[i] = (float)p[i];
+      for (int i = 0; i < EPL; ++i) v[i] = (moves >> i) & 1 ? (float)p[i] : 0.0f;
     } else {
       for (int j = 0; j < a.k; ++j) {
         const int ej = __builtin_amdgcn_readlane(e, q * a.k + j);

@@ -108,6 +108,7 @@ def backward(logits, ids, w, dw, kind, renorm=True, scale=1.0):
         else:
             d, a = np.zeros_like(l), np.zeros_like(l)
             d[at], a[at] = ds, da
-            out[t] = s * (d - (d * s).sum())
-            size[t] = s * (a + (a * s).sum())
+            finite = l < np.inf  # (+inf counts as a number that it does not move)
+            out[t] = s * (d - (d * s).sum()) * finite
+            size[t] = s * (a + (a * s).sum()) * finite
     return out, size

@@ -119,3 +119,30 @@ def test_capacity_by_slots_and_through_a_layout(T, E, k):
                                 else m.route_scored(p, xs.cuda(), sc))
                 want = oracle.capacity(ids.cpu().numpy(), w.cpu().numpy(), E, C)
                 assert (keep.cpu().numpy() == want).all(), (C, sc)
+
+
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,k", [(8, 2), (64, 3), (72, 6), (256, 8), (300, 1), (520, 12)])
+def test_infinite_logits_get_no_gradient(E, k, kind, renorm):
+    """None, one, two or all of a token's logits +inf, beside the largest number and finite ones."""
+    m = moe()
+    T = 67
+    x = make_logits(T, E, 3)
+    for t in range(T):
+        x[t, torch.randperm(E, generator=torch.Generator().manual_seed(t))[:t % 4]] = INF
+    x[5], x[6, :] = INF, torch.finfo(torch.float32).max
+    x[6, E // 2] = x[7, 0] = INF
+    x[8] = 1.0  # equal weights without any
+    p = m.Problem(T=T, H=64, E=E, k=k, I=64, renormalize=int(renorm))
+    sc = m.Scoring(kind, scale=2.5)
+    ids, w, _ = scored.route(numpy_of(x), k, kind, renorm=renorm, scale=2.5)
+    dw = torch.randn(T, k, generator=torch.Generator().manual_seed(9))
+    want, size = scored.backward(numpy_of(x), ids, w, numpy_of(dw), kind, renorm, 2.5)
+    got = m.route_scored_backward(p, x.cuda(), sc, torch.from_numpy(ids).cuda(),
+                                  torch.from_numpy(w).cuda(), dw.cuda()).cpu().double().numpy()
+    assert (got[x.numpy() == np.inf] == 0).all()
+    # as in test_gpu_scored.py
+    g = dw.abs().numpy().sum(1, keepdims=True)
+    tol = 4 * 2.0 ** -24 * size + 2.0 ** -24 * np.abs(want) + 2.0 ** -149 * (1 + 4 * g)
+    assert (np.abs(got - want) <= tol).all()

@@ -101,3 +101,17 @@ def test_fp4_levels_ties_and_scales():
         assert s.item() == byte, top
         if byte == 255:
             assert c.eq(0).all() and fp4.dequantize(c, s).isnan().all()
+
+
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+def test_infinite_logits_get_no_gradient(kind, renorm):
+    l = np.array([[0.5, INF, -1.0, INF, 2.0], [INF, 0.0, 1.0, scored.BIG, -INF]])
+    ids, w, _ = scored.route(l, 3, kind, renorm=renorm)
+    dw = np.array([[0.3, -1.2, 0.7], [1.1, 0.4, -0.9]])
+    got, size = scored.backward(l, ids, w, dw, kind, renorm)
+    assert (got[l == INF] == 0).all() and (size[l == INF] == 0).all()
+    if kind == "softmax":  # as for the largest number in its place, but for itself
+        low = np.minimum(l, scored.BIG)
+        want = scored.backward(low, ids, w, dw, kind, renorm)[0]
+        assert np.array_equal(got[l < INF], want[l < INF]) and want[1, 0] != 0 and got[1, 3] != 0
