@@ -111,6 +111,17 @@ __device__ __forceinline__ void fp4_finish4(const Fp4Args& g, int e, int r, int 
   *(uint2*)(g.y + o) = make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
 }
 
+// ---- grouped_fp4.hip
+enum Fp4Kernel { kStream = 0, kTile256, kTile128, kTile128Once };
+
+// Which kernel a call takes and into how many parts it cuts the reduction, from its sizes alone
+// (the row counts are on the device).  Heights are those for x in 4 bits; for 8 they are half.
+struct Fp4Plan {
+  Fp4Kernel kernel;
+  int split;
+};
+Fp4Plan fp4_plan(const moe_grouped& p, bool eight, bool gated);
+
 // ---- grouped_fp4_stream.hip: a few rows per expert
 hipError_t launch_fp4_stream(const Fp4Args& g, bool eight, hipStream_t s);
 

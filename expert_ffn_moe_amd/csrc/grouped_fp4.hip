@@ -727,41 +727,6 @@ int cu_count() {
   return n;
 }
 
-enum Fp4Kernel { kStream = 0, kTile256, kTile128, kTile128Once };
-
-// Which kernel a call takes and into how many parts it cuts the reduction, from its sizes alone
-// (the row counts are on the device).  Heights are those for x in 4 bits; for 8 they are half.
-struct Fp4Plan {
-  Fp4Kernel kernel;
-  int split;
-};
-Fp4Plan fp4_plan(const moe_grouped& p, bool eight, bool gated) {
-  const int64_t rows = p.R / p.E, active = std::min(p.E, std::max(p.R, 1));
-  const int stages = div_up(p.K, 256), big = eight ? 128 : 256;
-  // tiles, with half of the experts that have rows having one more than those need
-  auto tiles = [&](int bm, int bn) {
-    const int64_t mt = std::max<int64_t>(active, p.R / bm + (p.E > 1 ? active / 2 : 1));
-    return mt * div_up(p.N, gated ? bn / 2 : bn);
-  };
-  const int64_t n256 = tiles(big, 256), n128 = tiles(big / 2, 128);
-  // few rows, and few tiles or short reductions: latency.  (16 rows for each of 128 experts, 2048 ->
-  // 768 twice: 55 us, tiles 59; 8 for each of 64, 4096 -> 1408 twice: 91 and 79 us.  x in 8 bits: 1 for
-  // each of the 128: 40 and 33 us; 4 of one 7168 -> 4096: 15 us, tiles in 4 parts the same, 16 of
-  // it 18 and 15.)
-  if (rows <= (eight ? 4 : 16) && (n128 < 256 || (!eight && stages <= 8))) return {kStream, 1};
-  // (4 bits: 128 rows for each of 64 experts, 4096 -> 1408: 77 us, with 128-tiles 80; 96 rows: 69 and
-  // 62, with the non-temporal hint 58.  8 bits: 64 rows 108 and 123 us; 48 rows 97 and 100, with the
-  // hint 97.  One 4096 x 2048 x 2048, 128 tiles: 23 and 19 us; 4096 x 7168 x 4096, 256 tiles: 67
-  // and 80 us.)
-  if (16 * rows > 7 * big && n256 >= 192) return {kTile256, 1};
-  // the weights are read once: with the non-temporal hint (8 rows for each of 256 experts, 7168 -> 1024
-  // twice: 388 and 358 us)
-  if (n128 >= 256) return {8 * rows <= 3 * big ? kTile128Once : kTile128, 1};
-  // few tiles: long reductions in parts (128 x 7168 x 4096, 32 tiles: 26 us, in 4 parts 18; 512 rows,
-  // 128 tiles: 26.3, in 2 parts 25.6, in 4 28; 1024 x 2048 x 2048: 12, in 2 parts 18)
-  return {kTile128, (int)std::max<int64_t>(1, std::min<int64_t>(stages / 7, 256 / n128))};
-}
-
 // Adds the parts of a split reduction in order and finishes: 4 columns per thread.
 __global__ __launch_bounds__(256) void fp4_join_kernel(const Fp4Args g) {
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
@@ -804,6 +769,33 @@ void launch_tiles(const Fp4Args& g, Fp4Kernel kernel, hipStream_t s) {
 }
 
 }  // namespace
+
+Fp4Plan fp4_plan(const moe_grouped& p, bool eight, bool gated) {
+  const int64_t rows = p.R / p.E, active = std::min(p.E, std::max(p.R, 1));
+  const int stages = div_up(p.K, 256), big = eight ? 128 : 256;
+  // tiles, with half of the experts that have rows having one more than those need
+  auto tiles = [&](int bm, int bn) {
+    const int64_t mt = std::max<int64_t>(active, p.R / bm + (p.E > 1 ? active / 2 : 1));
+    return mt * div_up(p.N, gated ? bn / 2 : bn);
+  };
+  const int64_t n256 = tiles(big, 256), n128 = tiles(big / 2, 128);
+  // few rows, and few tiles or short reductions: latency.  (16 rows for each of 128 experts, 2048 ->
+  // 768 twice: 55 us, tiles 59; 8 for each of 64, 4096 -> 1408 twice: 91 and 79 us.  x in 8 bits: 1 for
+  // each of the 128: 40 and 33 us; 4 of one 7168 -> 4096: 15 us, tiles in 4 parts the same, 16 of
+  // it 18 and 15.)
+  if (rows <= (eight ? 4 : 16) && (n128 < 256 || (!eight && stages <= 8))) return {kStream, 1};
+  // (4 bits: 128 rows for each of 64 experts, 4096 -> 1408: 77 us, with 128-tiles 80; 96 rows: 69 and
+  // 62, with the non-temporal hint 58.  8 bits: 64 rows 108 and 123 us; 48 rows 97 and 100, with the
+  // hint 97.  One 4096 x 2048 x 2048, 128 tiles: 23 and 19 us; 4096 x 7168 x 4096, 256 tiles: 67
+  // and 80 us.)
+  if (16 * rows > 7 * big && n256 >= 192) return {kTile256, 1};
+  // the weights are read once: with the non-temporal hint (8 rows for each of 256 experts, 7168 -> 1024
+  // twice: 388 and 358 us)
+  if (n128 >= 256) return {8 * rows <= 3 * big ? kTile128Once : kTile128, 1};
+  // few tiles: long reductions in parts (128 x 7168 x 4096, 32 tiles: 26 us, in 4 parts 18; 512 rows,
+  // 128 tiles: 26.3, in 2 parts 25.6, in 4 28; 1024 x 2048 x 2048: 12, in 2 parts 18)
+  return {kTile128, (int)std::max<int64_t>(1, std::min<int64_t>(stages / 7, 256 / n128))};
+}
 
 // (for either type of x, with or without a second weight set)
 size_t grouped_fp4_ws_bytes(const moe_grouped& p) {
