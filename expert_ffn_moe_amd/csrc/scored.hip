@@ -8,9 +8,10 @@
 //
 // Choices are those of 64-bit scores and weights are computed in 64 bits and rounded once: a
 // choice next to a border, and the capacity's comparison of weights, do then not depend on how an
-// exponential was rounded to 32 bits.  Most choices are nowhere near a border: a token is first
-// taken in 32 bits, and again in 64 only where two of the values that decided lay closer than
-// their error bounds (or were equal, or an expert that is out would be needed).
+// exponential was rounded to 32 bits.  Most choices are nowhere near a border: with up to 256
+// experts, 8 choices and groups of whole lanes a token is first taken in 32 bits, and again in 64
+// only where two of the values that decided lay closer than their error bounds (or were equal, or
+// an expert that is out would be needed).  All others are taken in 64 bits alone.
 #include <algorithm>
 #include <initializer_list>
 
@@ -31,7 +32,7 @@ struct ScoredArgs {
   size_t plane;
   int S, T, E, k, renorm, score, n_group, topk_group, group_score;
   int vec;   // rows can be read in words of min(EPL, 4) values
-  int span;  // rows kernel: lanes of a group where it is 2^n whole lanes, else 0
+  int span;  // rows kernel under a group limit: the lanes of a group, 1, 2, 4 or 8
   double scale;
 };
 
@@ -386,8 +387,8 @@ __global__ __launch_bounds__(256) void scored_rows_kernel(const ScoredArgs a) {
       c[i] = a.bias ? s[i] : c[i];
     }
   }
-  bool unsure = grouped && a.span == 0;
-  if (grouped && a.span != 0) {
+  bool unsure = false;
+  if (grouped) {
     float v1 = -INFINITY, v2 = -INFINITY;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
@@ -490,8 +491,10 @@ __global__ __launch_bounds__(256) void scored_rows_kernel(const ScoredArgs a) {
   }
 }
 
-// A wavefront per token, for more experts or choices; in 64 bits throughout, whose arithmetic bounds
-// it (see above for both at the same size).
+// A wavefront per token, for more experts or choices or groups that are not whole lanes; in 64 bits
+// throughout, whose arithmetic and rounds of choice bound it.  16384 tokens with sigmoid scores and
+// a bias: 8 of 384 48 us, 10 of 512 53, 8 of 512 in 8 groups 65, 16 of 256 43 (25, 34, 34 and 17 MB
+// of logits are 5, 7, 7 and 3.5 us).
 template <int EPL>  // E <= 64 * EPL
 __global__ __launch_bounds__(256) void scored_wide_kernel(const ScoredArgs a) {
   __shared__ double s_val[4][64 * EPL];
@@ -689,12 +692,17 @@ hipError_t launch_route_scored(const moe_problem& p, const moe_scoring& sc, cons
                                uint8_t* keep, hipStream_t s) {
   ScoredArgs a{logits, bias, logits_out, ids, w, keep, (size_t)p.T * p.E, S, p.T, p.E, p.k,
                p.renormalize, sc.score, sc.n_group, sc.topk_group, sc.group_score, 0, 0, sc.scale};
-  if (p.E <= 256 && p.k <= 8) {
-    const int epl = p.E <= 64 ? 4 : p.E <= 128 ? 8 : 16, gs = p.E / sc.n_group;
+  const int lane_experts = p.E <= 64 ? 4 : p.E <= 128 ? 8 : 16, gs = p.E / sc.n_group;
+  const int span = gs % lane_experts == 0 ? gs / lane_experts : 0;
+  const bool lanes = span == 1 || span == 2 || span == 4 || span == 8;
+  // Groups that are not whole lanes go to the other kernel: here they would all be chosen in 64 bits,
+  // a token after the other (16384 tokens, 6 of 160 experts in 8 groups 43.6 us, there 35.2; 512
+  // tokens 24.9 and 7.7; one 8.3 and 6.6; 4 of 72 in 8: 25.7 and 21.9, 15.7 and 5.6, 5.9 and 4.8).
+  if (p.E <= 256 && p.k <= 8 && (lanes || sc.topk_group == sc.n_group)) {
+    const int epl = lane_experts;
     // (the wavefront-wide form that the kernel falls back to reads smaller words of the same rows)
     a.vec = words_ok(p.E, 4, {logits, bias});
-    const int span = gs % epl == 0 ? gs / epl : 0;
-    a.span = span == 1 || span == 2 || span == 4 || span == 8 ? span : 0;
+    a.span = span;
     const dim3 grid(div_up(p.T, 16)), block(256);
     const bool soft = sc.score == MOE_SCORE_SOFTMAX;
     if (epl == 4 && soft) hipLaunchKernelGGL((scored_rows_kernel<4, true>), grid, block, 0, s, a);
