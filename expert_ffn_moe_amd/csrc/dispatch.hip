@@ -297,7 +297,15 @@ __device__ __forceinline__ uint64_t cap_boundary(int cnt, int C, KeyAt key_at, C
   return prefix;
 }
 
-// The same from the highest bit in which two keys differ, for keys at hand in LDS: the weights'
+// Over the 16 lanes of a row, the same in each (all lanes must be active).
+__device__ __forceinline__ uint64_t row_max_u64(uint64_t v) {
+  v = max_u64(v, dpp_u64<kDppQuadXor1>(v));
+  v = max_u64(v, dpp_u64<kDppQuadXor2>(v));
+  v = max_u64(v, dpp_u64<kDppRowHalfMirror>(v));
+  return max_u64(v, dpp_u64<kDppRowMirror>(v));
+}
+
+// cap_boundary from the highest bit in which two keys differ, for keys at hand in LDS: the weights'
 // exponents hardly do, and a digit that all keys share is counted by as many atomics on one address.
 // low, high: the least and the largest of the keys that this thread has built (~0, 0 for none).
 template <class KeyAt>
@@ -358,7 +366,7 @@ __global__ __launch_bounds__(kCapThreads) void capacity_select_kernel(
 // The same without a layout of the candidates, for few tokens: an expert's block looks through all
 // slots, notes its own and then reads their weights, loads that do not wait for each other.  Up to
 // kCapRanked candidates are ranked by counting the keys ahead of each, more by their digits.
-// (4099 tokens, 6 of 160 experts: 12 us; the layout's three launches and the selection took 24.)
+// (4099 tokens, 6 of 160 experts: 13 us; the layout's three launches and the selection took 24.)
 constexpr int kCapDirectTokens = 8192;
 constexpr int kCapRanked = 256;
 __global__ __launch_bounds__(kCapThreads) void capacity_direct_kernel(

@@ -33,16 +33,12 @@ __device__ __forceinline__ uint64_t shfl_xor_u64(uint64_t v, int m) {
 
 __device__ __forceinline__ uint64_t max_u64(uint64_t a, uint64_t b) { return a > b ? a : b; }
 
-// All-reduce max over the 16 lanes of a row (all lanes must be active).
-__device__ __forceinline__ uint64_t row_max_u64(uint64_t v) {
+// All-reduce max over the 64 lanes of a wavefront (all lanes must be active).
+__device__ __forceinline__ uint64_t wave_max_u64(uint64_t v) {
   v = max_u64(v, dpp_u64<kDppQuadXor1>(v));
   v = max_u64(v, dpp_u64<kDppQuadXor2>(v));
   v = max_u64(v, dpp_u64<kDppRowHalfMirror>(v));
-  return max_u64(v, dpp_u64<kDppRowMirror>(v));
-}
-// Over the 64 lanes of a wavefront (all lanes must be active).
-__device__ __forceinline__ uint64_t wave_max_u64(uint64_t v) {
-  v = row_max_u64(v);
+  v = max_u64(v, dpp_u64<kDppRowMirror>(v));
   v = max_u64(v, shfl_xor_u64(v, 16));
   v = max_u64(v, shfl_xor_u64(v, 32));
   return v;
