@@ -106,15 +106,17 @@ struct Item {
 // come through registers (their rows need not be aligned): loaded with a stage's copies, stored
 // before the barrier behind which the stage is read, ordered so that one LDS read brings a lane
 // the words of all its fragments.
-// ONCE: the weights are read once (one M tile per expert), with the non-temporal hint.
+// ONCE: weight copies with the non-temporal hint, for the calls whose experts have one M tile each on
+// the average (fp4_plan).
 //
-// What bounds it: a 256 x 256 tile brings 64 KiB of codes and 4 KiB of scales to LDS per stage, and the
-// CUs together draw 10.4 to 11 TB/s from their L2s; copies alone, without products, take 70 to 80% of
-// the whole time of 16384 x 8192 x 8192.  3.2 PFLOP/s on ragged rows (131072 rows of 256 experts, 7168
-// -> 2048 twice, 2.4 ms), 4.0 on that dense product; the instruction alone reaches 8.2 (fp4, 32 x 32 x
-// 64; 16 x 16 x 128: 6.1) and 4.5 with x in 8 bits.  Few rows per expert: the weights' bytes, 5.7 TB/s
-// (1024 rows of 256 experts, 7168 -> 2048 twice: 690 us).  Few stages: latency, the first two stages
-// of an item being copied beside the last ones of the item before it.
+// What it takes: a 256 x 256 tile brings 64 KiB of codes and 4 KiB of scales to LDS per stage, and the
+// CUs together draw 10.4 to 11 TB/s from their L2s (a rate reached; that it is their limit has not
+// been shown).  Copies alone, without products, take 70 to 80% of the whole time of 16384 x 8192 x
+// 8192; an eighth of a scale row's line is used at a time.  3.2 PFLOP/s on ragged rows (131072 rows of
+// 256 experts, 7168 -> 2048 twice, 2.4 ms), 4.0 on that dense product; the instruction alone reaches
+// 8.2 (fp4, 32 x 32 x 64; 16 x 16 x 128: 6.1) and 4.5 with x in 8 bits.  Few rows per expert: the
+// weights' bytes, 5.7 TB/s (1024 rows of 256 experts, 7168 -> 2048 twice: 690 us).  Few stages:
+// latency, the first two stages of an item being copied beside the last ones of the item before it.
 template <bool EIGHT, bool GATHER, int BM, int WM, int WN, bool ONCE = false>
 __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2, 2)))
 void fp4_tile_kernel(const Fp4Args g) {
@@ -789,8 +791,12 @@ Fp4Plan fp4_plan(const moe_grouped& p, bool eight, bool gated) {
   // hint 97.  One 4096 x 2048 x 2048, 128 tiles: 23 and 19 us; 4096 x 7168 x 4096, 256 tiles: 67
   // and 80 us.)
   if (16 * rows > 7 * big && n256 >= 192) return {kTile256, 1};
-  // the weights are read once: with the non-temporal hint (8 rows for each of 256 experts, 7168 -> 1024
-  // twice: 388 and 358 us)
+  // weights that are read once for an expert's one tile: with the non-temporal hint (8 rows for each of
+  // 256 experts, 7168 -> 1024 twice: 388 and 358 us).  The average alone is known here: where skewed
+  // routing gives some experts several tiles the hint costs.  16384 rows of 256 experts, 7168 -> 2048
+  // twice, without and with it: even 908 and 889 us; half of the rows with experts of more than a tile
+  // 947 and 1003; nine tenths 666 and 744.  2048 -> 768 twice, 8192 rows of 128: 70 and 68,
+  // 69 and 69, 62 and 62.
   if (n128 >= 256) return {8 * rows <= 3 * big ? kTile128Once : kTile128, 1};
   // few tiles: long reductions in parts (128 x 7168 x 4096, 32 tiles: 26 us, in 4 parts 18; 512 rows,
   // 128 tiles: 26.3, in 2 parts 25.6, in 4 28; 1024 x 2048 x 2048: 12, in 2 parts 18)

@@ -556,8 +556,8 @@ struct ScoredBwdArgs {
 //   softmax                dl_e = [e chosen] w_e d_e - p_e sum w d
 // In 64 bits, for d_j - D cancels.  A wavefront takes a.tokens tokens: their slots first, one to a
 // lane, then their rows, a lane holding EPL consecutive experts.  Bound by the stores: 16384 x 256, 16.8
-// MB of gradient, 9.0 us a call (softmax over all experts, which reads the logits too and takes
-// their exponentials in 64 bits, 17 us).
+// MB of gradient, 9.1 us a call (softmax over all experts, which reads the logits too and takes
+// their exponentials in 64 bits, 18 us).
 template <int EPL>
 __global__ __launch_bounds__(256) void scored_bwd_kernel(const ScoredBwdArgs a) {
   const int lane = threadIdx.x & 63;

@@ -572,8 +572,8 @@ int moe_activation_backward(int64_t rows, int32_t cols, const int32_t* live_rows
  *                0: w = scale * s
  *   scale        > 0 and finite in 32 bits
  * Without a bias experts are ordered by their logits, with which the scores rise.  Ties go to the
- * lower expert (group) id.  Scores, choices and weights are computed in 64 bits, each weight
- * rounded once to f32.
+ * lower expert (group) id.  Scores, choices and weights are those of 64 bits, each weight rounded
+ * once to f32.
  *
  * An expert is out for a token where its logit is NaN or -inf, or its bias is (+inf counts as the
  * largest f32).  It takes no part in the group scores and the choice, with such a logit nor in
